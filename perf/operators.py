@@ -84,13 +84,14 @@ def draw(rng):
     if op == "few":
         E, k, n_group, topk_group = rng.choice(((8, 2, 1, 1), (16, 2, 1, 1), (64, 2, 1, 1), (64, 6, 8, 3), (256, 8, 8, 4), (96, 4, 1, 1)))
         presel = rng.choice((0, 0, 8)) if n_group == 1 else 0
-        return _few("", _log(rng, 1, 32), 64 * _log(rng, 8, 64), E, k, 64 * _log(rng, 3, 32), rng.choice(("bf16", "mxfp4")), n_group, topk_group,
-                    presel, rng.choice((0, 1)), rng.choice((0.0, 0.1)))
+        weights, unit = rng.choice((("bf16", 64), ("mxfp4", 128)))  # 4-bit products take whole 128-wide steps
+        return _few("", _log(rng, 1, 32), unit * _log(rng, 512 // unit, 4096 // unit), E, k, unit * _log(rng, 256 // unit, 2048 // unit), weights,
+                    n_group, topk_group, presel, rng.choice((0, 1)), rng.choice((0.0, 0.1)))
     if op == "payload":
         return _payload("", _log(rng, 1, 8192), 64 * _log(rng, 4, 112), rng.choice((8, 16, 64)), rng.choice((1, 2, 4)), rng.choice((0.0, 1.1)))
     if op == "product":
-        return _product("", rng.choice(("gate_up", "down")), _log(rng, 1, 6000), 64 * _log(rng, 8, 96), rng.choice((4, 8, 16, 33)), rng.choice((1, 2, 4)),
-                        64 * _log(rng, 3, 48), rng.choice((0.0, 1.1)))
+        return _product("", rng.choice(("gate_up", "down")), _log(rng, 1, 6000), 128 * _log(rng, 4, 48), rng.choice((4, 8, 16, 33)), rng.choice((1, 2, 4)),
+                        128 * _log(rng, 2, 24), rng.choice((0.0, 1.1)))
     dtype = rng.choice(("bf16", "bf16", "f32"))
     d = 64 * _log(rng, 2, 112) if dtype == "bf16" else 4 * _log(rng, 16, 1200)
     if op == "norm":
