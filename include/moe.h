@@ -8,6 +8,9 @@
  *                                                (both: moe_grouped_ffn)
  *   weighted combine back to token order      -> moe_combine
  *   all of the above in one call              -> moe_layer_fwd
+ *   the whole layer for 1..32 tokens          -> moe_layer_fwd_few
+ *   4-bit payload and expert products         -> moe_quantize_mxfp4, ...
+ *   norms around the block, gate, residual    -> moe_norm, moe_combine_norm
  *
  * Pages cited by title and section:
  *   [EP-V4]      "DeepSeek-V4的Expert Parallelism与计算通信遮掩实战解析" (tqpw.cn)
@@ -80,8 +83,19 @@ enum moe_entry {
   MOE_ENTRY_LAYER = 5,
   MOE_ENTRY_ROUTE_STATS = 6,
   MOE_ENTRY_FFN_BACKWARD = 7,
-  MOE_ENTRY_ROUTE_BACKWARD = 8
+  MOE_ENTRY_ROUTE_BACKWARD = 8,
+  MOE_ENTRY_LAYER_FEW = 9,
+  MOE_ENTRY_NORM_BACKWARD = 10
 };
+
+/* Which expert-weight images moe_layer_fwd_few reads. */
+enum moe_weights {
+  MOE_WEIGHTS_BF16 = 0, /* moe_pack_weights        */
+  MOE_WEIGHTS_MXFP4 = 1 /* moe_pack_weights_mxfp4  */
+};
+
+/* Most tokens of one moe_layer_fwd_few call. */
+#define MOE_FEW_MAX_TOKENS 32
 
 /*
  * Problem description.
@@ -548,6 +562,160 @@ int moe_route_backward(const moe_config* cfg, const void* x, const void* w_route
  */
 int moe_unpermute_backward(const moe_config* cfg, const void* d_x_perm, const int32_t* slot_of,
                            const void* d_x_router, void* d_x, void* stream);
+
+/*
+ * ---------------------------------------------------------------- MXFP4
+ * Microscaled 4-bit floating point: 32 consecutive elements of a row share a
+ * scale, a power of two held as its exponent plus 127 in one byte (255 = NaN);
+ * an element is a 4-bit code: sign, two exponent bits (bias 1), one mantissa
+ * bit, i.e. 0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives.  Two codes to a
+ * byte, the earlier element in the low nibble.  A row of n elements is n / 2
+ * code bytes and n / 32 scale bytes (17 / 32 byte an element).
+ */
+
+/*
+ * moe_quantize_mxfp4: x [T, d] (dtype) -> codes [T, d / 2], scales [T, d / 32].
+ *   scale = 2^(floor(log2 max|x|) - 2) over the block (at least 2^-127; 2^-127
+ *   for a block of zeros); code = x / scale to nearest, ties to the even code,
+ *   saturating at 6; -0 keeps its sign.  A block that holds an infinity or
+ *   NaN gets scale byte 255 and codes 0 (it decodes to NaN).
+ *   Any tensor of rows can be quantised: only T, d and dtype of cfg are used
+ *   (T rows of d elements; d a multiple of 32, MOE_EUNSUPPORTED otherwise).
+ *   Pointers 16-byte aligned (scales: 4).
+ * moe_dequantize_mxfp4: x_perm[p] = the values of row src_of[p] / k, [T*k, d]
+ *   (dtype) out -- or, with src_of NULL, of row p, [T, d] out.  Exact: every
+ *   code value is a bfloat16 (src_of is clamped into the batch).
+ */
+int moe_quantize_mxfp4(const moe_config* cfg, const void* x, uint8_t* codes, uint8_t* scales,
+                       void* stream);
+int moe_dequantize_mxfp4(const moe_config* cfg, const uint8_t* codes, const int32_t* src_of,
+                         const uint8_t* scales, void* x_perm, void* stream);
+
+/*
+ * Expert weights in MXFP4, blocks along each weight row (the k of its product):
+ * codes [E, f, d / 2] and scales [E, f, d / 32] of gate and up, [E, d, f / 2] and
+ * [E, d, f / 32] of down -- as moe_quantize_mxfp4 writes them for the [E*f, d] (or
+ * [E*d, f]) rows, or as a checkpoint holds them.  moe_pack_weights_mxfp4 lays
+ * them out once, at load time, in the order the kernels read (no values changed;
+ * experts in ID order, expert e0's share of an image starts at byte
+ * e0 * (bytes / E)).  d and f must be multiples of 128 and dtype
+ * MOE_BF16 (MOE_EUNSUPPORTED otherwise).
+ * moe_mxfp4_weight_bytes: bytes of the two images.
+ * moe_pack_weights_mxfp4: either image may be NULL (its inputs are then
+ *   ignored).  All pointers 16-byte aligned.
+ */
+int moe_mxfp4_weight_bytes(const moe_config* cfg, size_t* gate_up_bytes, size_t* down_bytes);
+int moe_pack_weights_mxfp4(const moe_config* cfg, const uint8_t* gate_codes,
+                           const uint8_t* gate_scales, const uint8_t* up_codes,
+                           const uint8_t* up_scales, const uint8_t* down_codes,
+                           const uint8_t* down_scales, void* image_gate_up, void* image_down,
+                           void* stream);
+
+/*
+ * Expert products on MXFP4 operands: the sums over k of the products of the
+ * decoded values, float32 accumulation; row-table and sub-table rules of
+ * moe_ffn_gate_up (the image advanced by e0 * (bytes / E)).
+ * moe_ffn_gate_up_mxfp4_gather: h[p] = SiLU(x_t Wg_e^T) (x_t Wu_e^T), t =
+ *   src_of[p] / k, on x's codes [T, d / 2] and scales [T, d / 32] in token order;
+ *   h [T*k, f] bf16 out.
+ * moe_ffn_down_mxfp4: y_perm[p] = h[p] Wd_e^T on h's codes [T*k, f / 2] and
+ *   scales [T*k, f / 32] (moe_quantize_mxfp4 with T*k rows of f elements);
+ *   y_perm [T*k, d] bf16 out.
+ * Rows outside the table are not touched.  Codes and outputs 16-byte, scales
+ * 4-byte aligned.
+ */
+int moe_ffn_gate_up_mxfp4_gather(const moe_config* cfg, const uint8_t* x_codes,
+                                 const uint8_t* x_scales, const int32_t* src_of,
+                                 const int32_t* expert_offsets, const void* image_gate_up,
+                                 void* h, void* stream);
+int moe_ffn_down_mxfp4(const moe_config* cfg, const uint8_t* h_codes, const uint8_t* h_scales,
+                       const int32_t* expert_offsets, const void* image_down, void* y_perm,
+                       void* stream);
+
+/*
+ * The whole layer for a few tokens (0 <= T <= MOE_FEW_MAX_TOKENS,
+ * MOE_EUNSUPPORTED above): decode steps and drafts checked at once, in two
+ * kernels.  Routing bit for bit as moe_route; out as moe_layer_fwd computes it,
+ * with h rounded to bf16 and the expert outputs left in float32 until the
+ * weighted sum is rounded once.
+ *   gate_up, down  the images of moe_pack_weights (weights ==
+ *                  MOE_WEIGHTS_BF16) or of moe_pack_weights_mxfp4
+ *                  (MOE_WEIGHTS_MXFP4: d and f multiples of 128; the
+ *                  activations stay bf16).  16-byte aligned.
+ *   bufs           NULL, or a moe_layer_bufs whose logits, topk_idx and topk_w
+ *                  are written where given; every other field must be NULL
+ *                  (MOE_EINVAL): the layer forms no dispatch.
+ *   ws             moe_workspace_bytes(MOE_ENTRY_LAYER_FEW).
+ * MOE_BF16 only.  Nothing in ws need be initialised or kept between calls.
+ */
+int moe_layer_fwd_few(const moe_config* cfg, const void* x, const void* w_router,
+                      const float* bias, const void* gate_up, const void* down, int weights,
+                      void* out, const moe_layer_bufs* bufs, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/*
+ * ---------------------------------------------------------------- norms
+ * RMS norms in front of and behind the block, the one behind fused with the
+ * combine, the block's gate and the scaled residual.  Both element types;
+ * statistics and sums in float32; rows of up to 16384 (bf16) or 8192 (f32)
+ * elements (MOE_EUNSUPPORTED above).  Tensors 16-byte aligned.  Only T, d, k
+ * and dtype of cfg are used.  rstd [T] float32 is kept for the backward.
+ */
+
+/*
+ * moe_norm: xn[t] = x[t] r w,  r = rstd[t] = 1 / sqrt(mean(x[t]^2) + eps).
+ *   x, xn [T, d] (dtype); weight [d] (dtype) or NULL (1); rstd out or NULL.
+ *   eps > 0 and finite.
+ * moe_norm_backward: with n = x r, c = mean(d_xn w n):
+ *   d_x[t] = (d_residual[t] if given) + r (d_xn w - n c)   [T, d] (dtype) out
+ *   d_weight = sum_t d_xn n                                 [d] float32 out or NULL
+ *   d_residual is the gradient that reaches x past the norm; d_x may be the
+ *   same buffer.  ws: moe_workspace_bytes(MOE_ENTRY_NORM_BACKWARD), needed
+ *   where d_weight is given.
+ */
+int moe_norm(const moe_config* cfg, const void* x, const void* weight, float eps, void* xn,
+             float* rstd, void* stream);
+int moe_norm_backward(const moe_config* cfg, const void* d_xn, const void* x, const void* weight,
+                      const float* rstd, const void* d_residual, void* d_x, float* d_weight,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_combine_norm: y[t] = sum_j topk_w[t,j] y_perm[slot_of[t*k+j]] (float32,
+ * never rounded), r = rstd[t] = 1 / sqrt(mean(y[t]^2) + eps),
+ *   out[t] = residual_scale residual[t] + gate[t / (T / n_gate)] (y[t] r weight).
+ *   y          [T*k, d] (dtype) expert rows; with slot_of and topk_w NULL it
+ *              is the layer's output in token order, [T, d] (after
+ *              moe_layer_fwd_few).
+ *   residual   [T, d] (dtype) or NULL (0); out may be the same buffer.
+ *   weight     [d] (dtype) or NULL (1).
+ *   gate       [n_gate, d] (dtype): n_gate divides T, each row gates T / n_gate
+ *              consecutive tokens (1: a learned scale per channel; the number of
+ *              sequences: one per sequence; T: one per token).  NULL with
+ *              n_gate = 0: 1.
+ * moe_combine_norm_backward: with n = y r, dn = gate weight d_out,
+ * dy = r (dn - n mean(dn n)):
+ *   d_y[slot_of[t*k+j]] = topk_w[t,j] dy     [T*k, d] (dtype) out ([T, d] = dy
+ *                                            with slot_of NULL)
+ *   d_topk_w[t,j] = <dy, y[slot_of[t*k+j]]>  [T, k] float32 out or NULL (must be
+ *                                            NULL with slot_of NULL)
+ *   d_residual = residual_scale d_out        [T, d] (dtype) out or NULL
+ *   d_weight = sum_t gate d_out n            [d] float32 out or NULL
+ *   d_gate[q] = weight sum of d_out n over the tokens of row q
+ *                                            [n_gate, d] float32 out or NULL
+ *   ws: moe_combine_norm_backward_bytes, needed where d_weight or d_gate is given.
+ * A malformed slot_of stays in bounds.
+ */
+int moe_combine_norm(const moe_config* cfg, const void* y, const int32_t* slot_of,
+                     const float* topk_w, const void* residual, const void* weight,
+                     const void* gate, int n_gate, float eps, float residual_scale, void* out,
+                     float* rstd, void* stream);
+int moe_combine_norm_backward_bytes(const moe_config* cfg, int n_gate, size_t* bytes);
+int moe_combine_norm_backward(const moe_config* cfg, const void* d_out, const void* y,
+                              const int32_t* slot_of, const float* topk_w, const void* weight,
+                              const void* gate, int n_gate, float residual_scale,
+                              const float* rstd, void* d_y, float* d_topk_w, void* d_residual,
+                              float* d_weight, float* d_gate, void* ws, size_t ws_bytes,
+                              void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,7 +19,9 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi35
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP, MOE_ESCRATCH = 0, -1, -2, -3, -4
 MOE_F32, MOE_BF16 = 0, 1
 ENTRY = {"route": 1, "permute": 2, "ffn": 3, "combine": 4, "layer": 5, "route_stats": 6,
-         "ffn_backward": 7, "route_backward": 8}
+         "ffn_backward": 7, "route_backward": 8, "layer_few": 9, "norm_backward": 10}
+MOE_WEIGHTS_BF16, MOE_WEIGHTS_MXFP4 = 0, 1
+MOE_FEW_MAX_TOKENS = 32
 
 CONFIG_FIELDS = ("T", "d", "E", "k", "f", "n_group", "topk_group", "presel", "renorm",
                  "ep_ranks", "dtype")
@@ -36,7 +38,10 @@ EXPORTS = ("moe_strerror", "moe_validate", "moe_workspace_bytes", "moe_route", "
            "moe_ffn_gate_up_packed_train", "moe_packed_weight_bytes_backward",
            "moe_pack_weights_backward", "moe_permute_noalloc", "moe_noalloc_scratch_bytes",
            "moe_fp8_weight_bytes", "moe_pack_weights_fp8", "moe_ffn_gate_up_fp8_gather",
-           "moe_layer_fwd_packed_waved")
+           "moe_layer_fwd_packed_waved", "moe_quantize_mxfp4", "moe_dequantize_mxfp4",
+           "moe_mxfp4_weight_bytes", "moe_pack_weights_mxfp4", "moe_ffn_gate_up_mxfp4_gather",
+           "moe_ffn_down_mxfp4", "moe_layer_fwd_few", "moe_norm", "moe_norm_backward",
+           "moe_combine_norm", "moe_combine_norm_backward_bytes", "moe_combine_norm_backward")
 
 
 class MoEConfig(ctypes.Structure):
@@ -104,6 +109,21 @@ def lib() -> ctypes.CDLL:
                                            ctypes.POINTER(MoELayerBufs), vp, sz, vp]
         L.moe_layer_fwd_packed_waved.argtypes = [cfgp, vp, vp, vp, vp, vp, vp,
                                                  ctypes.POINTER(MoELayerBufs), vp, sz, i32, vp, vp]
+        f32 = ctypes.c_float
+        L.moe_quantize_mxfp4.argtypes = [cfgp, vp, vp, vp, vp]
+        L.moe_dequantize_mxfp4.argtypes = [cfgp, vp, vp, vp, vp, vp]
+        L.moe_mxfp4_weight_bytes.argtypes = [cfgp, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+        L.moe_pack_weights_mxfp4.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_ffn_gate_up_mxfp4_gather.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_ffn_down_mxfp4.argtypes = [cfgp, vp, vp, vp, vp, vp, vp]
+        L.moe_layer_fwd_few.argtypes = [cfgp, vp, vp, vp, vp, vp, i32, vp,
+                                        ctypes.POINTER(MoELayerBufs), vp, sz, vp]
+        L.moe_norm.argtypes = [cfgp, vp, vp, f32, vp, vp, vp]
+        L.moe_norm_backward.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_combine_norm.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, i32, f32, f32, vp, vp, vp]
+        L.moe_combine_norm_backward_bytes.argtypes = [cfgp, i32, ctypes.POINTER(sz)]
+        L.moe_combine_norm_backward.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, i32, f32, vp, vp, vp,
+                                                vp, vp, vp, vp, sz, vp]
         for name in EXPORTS[1:]:
             getattr(L, name).restype = i32
         L.moe_noalloc_scratch_bytes.restype = sz
@@ -403,6 +423,122 @@ def moe_layer_fwd_packed(cfg, x, w_router, bias, packed_gate_up, packed_down, ou
            lib().moe_layer_fwd_packed(ctypes.byref(cfg), _ptr(x), _ptr(w_router), _ptr(bias),
                                       _ptr(packed_gate_up), _ptr(packed_down), _ptr(out),
                                       ctypes.byref(b) if b else None, wp, wn, _stream(stream)))
+
+
+def moe_quantize_mxfp4(cfg, x, codes, scales, stream=None):
+    _check("moe_quantize_mxfp4", lib().moe_quantize_mxfp4(ctypes.byref(cfg), _ptr(x), _ptr(codes),
+                                                          _ptr(scales), _stream(stream)))
+
+
+def quantize_mxfp4(x, stream=None):
+    """Allocates and fills the MXFP4 codes and scales of a tensor's rows (bf16
+    or float32, last dimension a multiple of 64): ([..., n / 2], [..., n / 32])."""
+    n = x.shape[-1]
+    cfg = config(T=x.numel() // n, d=n, E=1, k=1, f=64,
+                 dtype=MOE_BF16 if x.dtype == torch.bfloat16 else MOE_F32)
+    codes = torch.empty((*x.shape[:-1], n // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((*x.shape[:-1], n // 32), dtype=torch.uint8, device=x.device)
+    moe_quantize_mxfp4(cfg, x, codes, scales, stream)
+    return codes, scales
+
+
+def moe_dequantize_mxfp4(cfg, codes, src_of, scales, x_perm, stream=None):
+    _check("moe_dequantize_mxfp4",
+           lib().moe_dequantize_mxfp4(ctypes.byref(cfg), _ptr(codes), _ptr(src_of), _ptr(scales),
+                                      _ptr(x_perm), _stream(stream)))
+
+
+def mxfp4_weight_bytes(cfg) -> tuple[int, int]:
+    gu, dn = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check("moe_mxfp4_weight_bytes",
+           lib().moe_mxfp4_weight_bytes(ctypes.byref(cfg), ctypes.byref(gu), ctypes.byref(dn)))
+    return gu.value, dn.value
+
+
+def moe_pack_weights_mxfp4(cfg, gate_codes, gate_scales, up_codes, up_scales, down_codes,
+                           down_scales, image_gate_up, image_down, stream=None):
+    _check("moe_pack_weights_mxfp4",
+           lib().moe_pack_weights_mxfp4(ctypes.byref(cfg), _ptr(gate_codes), _ptr(gate_scales),
+                                        _ptr(up_codes), _ptr(up_scales), _ptr(down_codes),
+                                        _ptr(down_scales), _ptr(image_gate_up), _ptr(image_down),
+                                        _stream(stream)))
+
+
+def pack_weights_mxfp4(cfg, gate, up, down, device="cuda", stream=None):
+    """Allocates and fills the MXFP4 images from (codes, scales) pairs; an image
+    whose weights are None is neither allocated nor written (None)."""
+    gu, dn = mxfp4_weight_bytes(cfg)
+    pgu = torch.empty(gu, dtype=torch.uint8, device=device) if gate is not None else None
+    pd = torch.empty(dn, dtype=torch.uint8, device=device) if down is not None else None
+    none = (None, None)
+    moe_pack_weights_mxfp4(cfg, *(gate or none), *(up or none), *(down or none), pgu, pd, stream)
+    return pgu, pd
+
+
+def moe_ffn_gate_up_mxfp4_gather(cfg, x_codes, x_scales, src_of, expert_offsets, image, h,
+                                 stream=None):
+    _check("moe_ffn_gate_up_mxfp4_gather", lib().moe_ffn_gate_up_mxfp4_gather(
+        ctypes.byref(cfg), _ptr(x_codes), _ptr(x_scales), _ptr(src_of), _ptr(expert_offsets),
+        _ptr(image), _ptr(h), _stream(stream)))
+
+
+def moe_ffn_down_mxfp4(cfg, h_codes, h_scales, expert_offsets, image, y_perm, stream=None):
+    _check("moe_ffn_down_mxfp4", lib().moe_ffn_down_mxfp4(
+        ctypes.byref(cfg), _ptr(h_codes), _ptr(h_scales), _ptr(expert_offsets), _ptr(image),
+        _ptr(y_perm), _stream(stream)))
+
+
+def moe_layer_fwd_few(cfg, x, w_router, bias, gate_up, down, weights, out,
+                      bufs: dict | None = None, ws=None, stream=None):
+    b = None
+    if bufs:
+        b = MoELayerBufs(**{n: _ptr(bufs.get(n)) for n in LAYER_BUF_FIELDS})
+    wp, wn = _ws(ws)
+    _check("moe_layer_fwd_few", lib().moe_layer_fwd_few(
+        ctypes.byref(cfg), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(gate_up), _ptr(down),
+        int(weights), _ptr(out), ctypes.byref(b) if b else None, wp, wn, _stream(stream)))
+
+
+def moe_norm(cfg, x, weight, eps, xn, rstd=None, stream=None):
+    _check("moe_norm", lib().moe_norm(ctypes.byref(cfg), _ptr(x), _ptr(weight), eps, _ptr(xn),
+                                      _ptr(rstd), _stream(stream)))
+
+
+def moe_norm_backward(cfg, d_xn, x, weight, rstd, d_residual, d_x, d_weight, ws=None, stream=None):
+    wp, wn = _ws(ws)
+    _check("moe_norm_backward", lib().moe_norm_backward(
+        ctypes.byref(cfg), _ptr(d_xn), _ptr(x), _ptr(weight), _ptr(rstd), _ptr(d_residual),
+        _ptr(d_x), _ptr(d_weight), wp, wn, _stream(stream)))
+
+
+def moe_combine_norm(cfg, y, slot_of, topk_w, residual, weight, gate, n_gate, eps, residual_scale,
+                     out, rstd=None, stream=None):
+    _check("moe_combine_norm", lib().moe_combine_norm(
+        ctypes.byref(cfg), _ptr(y), _ptr(slot_of), _ptr(topk_w), _ptr(residual), _ptr(weight),
+        _ptr(gate), int(n_gate), eps, residual_scale, _ptr(out), _ptr(rstd), _stream(stream)))
+
+
+def combine_norm_backward_bytes(cfg, n_gate) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_combine_norm_backward_bytes",
+           lib().moe_combine_norm_backward_bytes(ctypes.byref(cfg), int(n_gate), ctypes.byref(n)))
+    return n.value
+
+
+def combine_norm_workspace(cfg, n_gate, device="cuda") -> torch.Tensor | None:
+    """A caller-owned workspace for moe_combine_norm_backward with n_gate gate rows."""
+    n = combine_norm_backward_bytes(cfg, n_gate)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def moe_combine_norm_backward(cfg, d_out, y, slot_of, topk_w, weight, gate, n_gate,
+                              residual_scale, rstd, d_y, d_topk_w, d_residual, d_weight, d_gate,
+                              ws=None, stream=None):
+    wp, wn = _ws(ws)
+    _check("moe_combine_norm_backward", lib().moe_combine_norm_backward(
+        ctypes.byref(cfg), _ptr(d_out), _ptr(y), _ptr(slot_of), _ptr(topk_w), _ptr(weight),
+        _ptr(gate), int(n_gate), residual_scale, _ptr(rstd), _ptr(d_y), _ptr(d_topk_w),
+        _ptr(d_residual), _ptr(d_weight), _ptr(d_gate), wp, wn, _stream(stream)))
 
 
 # ------------------------------------------------------------ device tensors

@@ -2,6 +2,8 @@
 // checks, workspace layout and the launch sequence of each entry point.
 // Nothing here allocates, frees or synchronises; every check runs before the
 // first launch, so a rejected call writes no output.
+#include <cmath>
+#include <initializer_list>
 #include <vector>
 
 #include "common.h"
@@ -164,6 +166,38 @@ int check_packed(const moe_config* c) {
 size_t packed_bytes(const moe_config& c, bool gate_up) {
   const PackGeom g = gate_up ? pack_geom(c.f, c.d, true) : pack_geom(c.d, c.f, false);
   return (size_t)c.E * g.expert_elems * 2;
+}
+
+bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
+// Rows that fit the norm kernels' registers.
+int check_norm(const moe_config* c) {
+  int s = check_core(c);
+  if (s != MOE_OK) return s;
+  return norm_row_supported(*c) ? MOE_OK : MOE_EUNSUPPORTED;
+}
+
+// n_gate gate rows, each for T / n_gate consecutive tokens (0: no gate).
+int check_gate(const moe_config& c, const void* gate, int n_gate) {
+  if (n_gate < 0 || (n_gate > 0 && c.T % n_gate)) return MOE_EINVAL;
+  if (!gate != (n_gate == 0)) return MOE_EINVAL;
+  if (n_gate > 0 && c.d > kI32Max / n_gate) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+// MXFP4 expert products: whole 128-wide k steps in both directions.
+int check_mxfp4(const moe_config* c) {
+  int s = check_packed(c);
+  if (s != MOE_OK) return s;
+  return c->d % 128 || c->f % 128 ? MOE_EUNSUPPORTED : MOE_OK;
+}
+
+int check_few(const moe_config* c, int weights) {
+  int s = check_routing(c);
+  if (s != MOE_OK) return s;
+  if (weights != MOE_WEIGHTS_BF16 && weights != MOE_WEIGHTS_MXFP4) return MOE_EINVAL;
+  if ((s = weights == MOE_WEIGHTS_MXFP4 ? check_mxfp4(c) : check_packed(c)) != MOE_OK) return s;
+  return c->T > kFewMaxTokens ? MOE_EUNSUPPORTED : MOE_OK;
 }
 
 int do_combine(const moe_config& c, const void* y, const int32_t* slot, const float* w, void* out,
@@ -337,6 +371,14 @@ int moe_workspace_bytes(const moe_config* cfg, int entry, size_t* bytes) {
     case MOE_ENTRY_ROUTE_BACKWARD:
       if ((s = check_routing(cfg)) != MOE_OK) return s;
       *bytes = align256(route_backward_ws_bytes(*cfg));
+      return MOE_OK;
+    case MOE_ENTRY_LAYER_FEW:
+      if ((s = check_few(cfg, MOE_WEIGHTS_BF16)) != MOE_OK) return s;
+      *bytes = few_ws_bytes(*cfg);
+      return MOE_OK;
+    case MOE_ENTRY_NORM_BACKWARD:
+      if ((s = check_norm(cfg)) != MOE_OK) return s;
+      *bytes = align256(norm_backward_ws_bytes(*cfg));
       return MOE_OK;
     default:
       return MOE_EINVAL;
@@ -732,6 +774,189 @@ int moe_unpermute_backward(const moe_config* cfg, const void* d_x_perm, const in
     return MOE_EINVAL;
   return status_of(launch_unpermute_backward(*cfg, d_x_perm, slot_of, d_x_router, d_x,
                                              static_cast<hipStream_t>(stream)));
+}
+
+int moe_quantize_mxfp4(const moe_config* cfg, const void* x, uint8_t* codes, uint8_t* scales,
+                       void* stream) {
+  int s = check_core(cfg);
+  if (s != MOE_OK) return s;
+  if (!mx_rows_supported(*cfg)) return MOE_EUNSUPPORTED;
+  if (cfg->T == 0) return MOE_OK;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned4(scales))
+    return MOE_EINVAL;
+  return status_of(launch_mx_quantize(*cfg, x, codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+int moe_dequantize_mxfp4(const moe_config* cfg, const uint8_t* codes, const int32_t* src_of,
+                         const uint8_t* scales, void* x_perm, void* stream) {
+  int s = check_core(cfg);
+  if (s != MOE_OK) return s;
+  if (!mx_rows_supported(*cfg)) return MOE_EUNSUPPORTED;
+  if (cfg->T == 0) return MOE_OK;
+  if (!codes || !scales || !x_perm || !aligned16(codes) || !aligned4(scales) ||
+      !aligned16(x_perm))
+    return MOE_EINVAL;
+  return status_of(launch_mx_dequantize(*cfg, codes, src_of, scales, x_perm,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int moe_mxfp4_weight_bytes(const moe_config* cfg, size_t* gate_up_bytes, size_t* down_bytes) {
+  int s = check_mxfp4(cfg);
+  if (s != MOE_OK) return s;
+  if (!gate_up_bytes || !down_bytes) return MOE_EINVAL;
+  *gate_up_bytes = mx_image_bytes(*cfg, true);
+  *down_bytes = mx_image_bytes(*cfg, false);
+  return MOE_OK;
+}
+
+int moe_pack_weights_mxfp4(const moe_config* cfg, const uint8_t* gate_codes,
+                           const uint8_t* gate_scales, const uint8_t* up_codes,
+                           const uint8_t* up_scales, const uint8_t* down_codes,
+                           const uint8_t* down_scales, void* image_gate_up, void* image_down,
+                           void* stream) {
+  int s = check_mxfp4(cfg);
+  if (s != MOE_OK) return s;
+  if (!image_gate_up && !image_down) return MOE_EINVAL;
+  const void* gu[] = {gate_codes, gate_scales, up_codes, up_scales, image_gate_up};
+  const void* dn[] = {down_codes, down_scales, image_down};
+  if (image_gate_up)
+    for (const void* p : gu)
+      if (!p || !aligned16(p)) return MOE_EINVAL;
+  if (image_down)
+    for (const void* p : dn)
+      if (!p || !aligned16(p)) return MOE_EINVAL;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (image_gate_up && launch_pack_weights_mxfp4(*cfg, gate_codes, gate_scales, up_codes,
+                                                 up_scales, true, image_gate_up, st) != hipSuccess)
+    return MOE_EHIP;
+  if (image_down && launch_pack_weights_mxfp4(*cfg, down_codes, down_scales, nullptr, nullptr,
+                                              false, image_down, st) != hipSuccess)
+    return MOE_EHIP;
+  return MOE_OK;
+}
+
+int moe_ffn_gate_up_mxfp4_gather(const moe_config* cfg, const uint8_t* x_codes,
+                                 const uint8_t* x_scales, const int32_t* src_of,
+                                 const int32_t* expert_offsets, const void* image_gate_up,
+                                 void* h, void* stream) {
+  int s = check_mxfp4(cfg);
+  if (s != MOE_OK) return s;
+  if (cfg->T == 0) return MOE_OK;
+  if (!x_codes || !x_scales || !src_of || !expert_offsets || !image_gate_up || !h ||
+      !aligned16(x_codes) || !aligned4(x_scales) || !aligned16(image_gate_up) || !aligned16(h))
+    return MOE_EINVAL;
+  return status_of(launch_ffn_gate_up_mxfp4(*cfg, x_codes, x_scales, src_of, expert_offsets,
+                                            image_gate_up, h, static_cast<hipStream_t>(stream)));
+}
+
+int moe_ffn_down_mxfp4(const moe_config* cfg, const uint8_t* h_codes, const uint8_t* h_scales,
+                       const int32_t* expert_offsets, const void* image_down, void* y_perm,
+                       void* stream) {
+  int s = check_mxfp4(cfg);
+  if (s != MOE_OK) return s;
+  if (cfg->T == 0) return MOE_OK;
+  if (!h_codes || !h_scales || !expert_offsets || !image_down || !y_perm || !aligned16(h_codes) ||
+      !aligned4(h_scales) || !aligned16(image_down) || !aligned16(y_perm))
+    return MOE_EINVAL;
+  return status_of(launch_ffn_down_mxfp4(*cfg, h_codes, h_scales, expert_offsets, image_down,
+                                         y_perm, static_cast<hipStream_t>(stream)));
+}
+
+int moe_layer_fwd_few(const moe_config* cfg, const void* x, const void* w_router,
+                      const float* bias, const void* gate_up, const void* down, int weights,
+                      void* out, const moe_layer_bufs* bufs, void* ws, size_t ws_bytes,
+                      void* stream) {
+  int s = check_few(cfg, weights);
+  if (s != MOE_OK) return s;
+  if (bufs && (bufs->expert_offsets || bufs->rank_offsets || bufs->slot_of || bufs->src_of ||
+               bufs->x_perm || bufs->h || bufs->y_perm))
+    return MOE_EINVAL;
+  if (cfg->T == 0) return MOE_OK;
+  if (!x || !w_router || !gate_up || !down || !out || !aligned16(x) || !aligned16(w_router) ||
+      !aligned16(gate_up) || !aligned16(down) || !aligned16(out))
+    return MOE_EINVAL;
+  if ((s = check_ws(few_ws_bytes(*cfg), ws, ws_bytes)) != MOE_OK) return s;
+  return status_of(launch_layer_few(*cfg, x, w_router, bias, gate_up, down,
+                                    weights == MOE_WEIGHTS_MXFP4, out,
+                                    bufs ? bufs->logits : nullptr, bufs ? bufs->topk_idx : nullptr,
+                                    bufs ? bufs->topk_w : nullptr, ws,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+int moe_norm(const moe_config* cfg, const void* x, const void* weight, float eps, void* xn,
+             float* rstd, void* stream) {
+  int s = check_norm(cfg);
+  if (s != MOE_OK) return s;
+  if (!(eps > 0.f) || !std::isfinite(eps)) return MOE_EINVAL;
+  if (cfg->T == 0) return MOE_OK;
+  if (!x || !xn || !aligned16(x) || !aligned16(weight) || !aligned16(xn)) return MOE_EINVAL;
+  return status_of(launch_norm(*cfg, x, weight, eps, xn, rstd, static_cast<hipStream_t>(stream)));
+}
+
+int moe_norm_backward(const moe_config* cfg, const void* d_xn, const void* x, const void* weight,
+                      const float* rstd, const void* d_residual, void* d_x, float* d_weight,
+                      void* ws, size_t ws_bytes, void* stream) {
+  int s = check_norm(cfg);
+  if (s != MOE_OK) return s;
+  if (cfg->T > 0) {
+    if (!d_xn || !x || !rstd || !d_x) return MOE_EINVAL;
+    for (const void* p : {d_xn, x, weight, d_residual, static_cast<const void*>(d_x)})
+      if (!aligned16(p)) return MOE_EINVAL;
+    if (d_weight && (s = check_ws(norm_backward_ws_bytes(*cfg), ws, ws_bytes)) != MOE_OK) return s;
+  }
+  return status_of(launch_norm_backward(*cfg, d_xn, x, weight, rstd, d_residual, d_x, d_weight, ws,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int moe_combine_norm(const moe_config* cfg, const void* y, const int32_t* slot_of,
+                     const float* topk_w, const void* residual, const void* weight,
+                     const void* gate, int n_gate, float eps, float residual_scale, void* out,
+                     float* rstd, void* stream) {
+  int s = check_norm(cfg);
+  if (s != MOE_OK) return s;
+  if ((s = check_gate(*cfg, gate, n_gate)) != MOE_OK) return s;
+  if (!(eps > 0.f) || !std::isfinite(eps) || !std::isfinite(residual_scale)) return MOE_EINVAL;
+  if (cfg->T == 0) return MOE_OK;
+  if (!y || !out || !slot_of != !topk_w) return MOE_EINVAL;
+  for (const void* p : {y, residual, weight, gate, static_cast<const void*>(out)})
+    if (!aligned16(p)) return MOE_EINVAL;
+  return status_of(launch_combine_norm(*cfg, y, slot_of, topk_w, residual, weight, gate, n_gate,
+                                       eps, residual_scale, out, rstd,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+int moe_combine_norm_backward_bytes(const moe_config* cfg, int n_gate, size_t* bytes) {
+  int s = check_norm(cfg);
+  if (s != MOE_OK) return s;
+  if (!bytes) return MOE_EINVAL;
+  if (n_gate < 0 || (n_gate > 0 && cfg->T % n_gate)) return MOE_EINVAL;
+  *bytes = align256(combine_norm_backward_ws_bytes(*cfg, n_gate));
+  return MOE_OK;
+}
+
+int moe_combine_norm_backward(const moe_config* cfg, const void* d_out, const void* y,
+                              const int32_t* slot_of, const float* topk_w, const void* weight,
+                              const void* gate, int n_gate, float residual_scale,
+                              const float* rstd, void* d_y, float* d_topk_w, void* d_residual,
+                              float* d_weight, float* d_gate, void* ws, size_t ws_bytes,
+                              void* stream) {
+  int s = check_norm(cfg);
+  if (s != MOE_OK) return s;
+  if ((s = check_gate(*cfg, gate, n_gate)) != MOE_OK) return s;
+  if (!std::isfinite(residual_scale) || (d_gate && !gate)) return MOE_EINVAL;
+  if (!slot_of != !topk_w || (d_topk_w && !slot_of)) return MOE_EINVAL;
+  if (cfg->T > 0) {
+    if (!d_out || !y || !rstd || !d_y) return MOE_EINVAL;
+    for (const void* p : {d_out, y, weight, gate, static_cast<const void*>(d_y),
+                          static_cast<const void*>(d_residual)})
+      if (!aligned16(p)) return MOE_EINVAL;
+    if ((d_weight || d_gate) &&
+        (s = check_ws(combine_norm_backward_ws_bytes(*cfg, n_gate), ws, ws_bytes)) != MOE_OK)
+      return s;
+  }
+  return status_of(launch_combine_norm_backward(
+      *cfg, d_out, y, slot_of, topk_w, weight, gate, n_gate, residual_scale, rstd, d_y, d_topk_w,
+      d_residual, d_weight, d_gate, ws, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -50,7 +50,8 @@ inline int div_up(long a, long b) { return (int)((a + b - 1) / b); }
 // Every launcher returns hipSuccess or the launch error; shapes are validated
 // by the C-ABI layer before these are called.
 hipError_t launch_router_gemm_bf16(const uint16_t* x, const uint16_t* wr, float* dst, int T, int d,
-                                   int E, int splits, hipStream_t st);
+                                   int E, int splits, hipStream_t st, uint32_t* clear = nullptr,
+                                   int n_clear = 0);
 hipError_t launch_router_gemm_f32(const float* x, const float* wr, float* dst, int T, int d, int E,
                                   hipStream_t st);
 hipError_t launch_topk(const moe_config& c, const float* partial, int splits, const float* bias,
@@ -70,6 +71,8 @@ hipError_t launch_ffn_gate_up(const moe_config& c, const void* x_perm, const int
                               const void* wg, const void* wu, void* h, hipStream_t st);
 hipError_t launch_ffn_down(const moe_config& c, const void* h, const int32_t* offs, const void* wd,
                            void* y, hipStream_t st);
+
+int device_cus();  // compute units of the current device
 
 // Packed expert weights (MFMA fragment order, zero padded; see ffn_packed.hip).
 struct PackGeom {
@@ -155,5 +158,49 @@ hipError_t launch_route_backward(const moe_config& c, const void* x, const void*
 hipError_t launch_unpermute_backward(const moe_config& c, const void* d_x_perm,
                                      const int32_t* slot_of, const void* d_x_router, void* d_x,
                                      hipStream_t st);
+
+// Norms around the block (norm.hip); either element type.
+bool norm_row_supported(const moe_config& c);
+size_t norm_backward_ws_bytes(const moe_config& c);
+size_t combine_norm_backward_ws_bytes(const moe_config& c, int n_gate);
+hipError_t launch_norm(const moe_config& c, const void* x, const void* w, float eps, void* xn,
+                       float* rstd, hipStream_t st);
+hipError_t launch_norm_backward(const moe_config& c, const void* d_xn, const void* x,
+                                const void* w, const float* rstd, const void* d_residual,
+                                void* d_x, float* d_w, void* ws, hipStream_t st);
+hipError_t launch_combine_norm(const moe_config& c, const void* y, const int32_t* slot_of,
+                               const float* topk_w, const void* residual, const void* w,
+                               const void* gate, int n_gate, float eps, float res_scale, void* out,
+                               float* rstd, hipStream_t st);
+hipError_t launch_combine_norm_backward(const moe_config& c, const void* d_out, const void* y,
+                                        const int32_t* slot_of, const float* topk_w, const void* w,
+                                        const void* gate, int n_gate, float res_scale,
+                                        const float* rstd, void* d_y, float* d_topk_w,
+                                        void* d_residual, float* d_w, float* d_gate, void* ws,
+                                        hipStream_t st);
+
+// MXFP4 payload, images and expert products (mxfp4.hip, ffn_mxfp4.hip).
+bool mx_rows_supported(const moe_config& c);
+hipError_t launch_mx_quantize(const moe_config& c, const void* x, void* codes, void* scales,
+                              hipStream_t st);
+hipError_t launch_mx_dequantize(const moe_config& c, const void* codes, const int32_t* src_of,
+                                const void* scales, void* x_perm, hipStream_t st);
+size_t mx_image_bytes(const moe_config& c, bool gate_up);
+hipError_t launch_pack_weights_mxfp4(const moe_config& c, const void* c0, const void* s0,
+                                     const void* c1, const void* s1, bool gate_up, void* image,
+                                     hipStream_t st);
+hipError_t launch_ffn_gate_up_mxfp4(const moe_config& c, const void* x_codes, const void* x_scales,
+                                    const int32_t* src_of, const int32_t* offs, const void* image,
+                                    void* h, hipStream_t st);
+hipError_t launch_ffn_down_mxfp4(const moe_config& c, const void* h_codes, const void* h_scales,
+                                 const int32_t* offs, const void* image, void* y, hipStream_t st);
+
+// The layer for a few tokens (few.hip); mx: MXFP4 images, else bf16 images.
+constexpr int kFewMaxTokens = MOE_FEW_MAX_TOKENS;
+size_t few_ws_bytes(const moe_config& c);
+hipError_t launch_layer_few(const moe_config& c, const void* x, const void* w_router,
+                            const float* bias, const void* gate_up, const void* down, bool mx,
+                            void* out, float* logits, int32_t* topk_idx, float* topk_w, void* ws,
+                            hipStream_t st);
 
 }  // namespace moe

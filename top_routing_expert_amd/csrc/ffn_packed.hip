@@ -758,7 +758,7 @@ hipError_t launch_pack_weights(const moe_config& c, const void* wg, const void* 
 }
 
 // Compute units of the current device (cached per device).
-static int device_cus() {
+int device_cus() {
   static int cached[64];
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;

@@ -21,10 +21,9 @@
 //    score bits, then inverted index), reduced with xor shuffles: highest
 //    score wins, ties go to the lowest expert index.
 #include "common.h"
+#include "topk.h"
 
 namespace moe {
-
-constexpr int kMaxSplits = 16;  // split-K partials of the router GEMM (summed by top-k)
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
@@ -37,7 +36,9 @@ template <int EC>
 __global__ __launch_bounds__(256) void router_gemm_bf16_kernel(const uint16_t* __restrict__ x,
                                                                const uint16_t* __restrict__ wr,
                                                                float* __restrict__ dst, int T, int d,
-                                                               int E, int splits) {
+                                                               int E, int splits,
+                                                               uint32_t* __restrict__ clear,
+                                                               int n_clear) {
   constexpr int NF = EC / 16;                         // expert fragments per wave
   constexpr int WLOADS = (EC * 8 + 255) / 256;        // 16-byte pieces per thread per chunk
   __shared__ u32x4 sW[2][EC * 8];
@@ -133,6 +134,8 @@ __global__ __launch_bounds__(256) void router_gemm_bf16_kernel(const uint16_t* _
       }
     }
   }
+  if (clear && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+    for (int i = threadIdx.x; i < n_clear; i += 256) clear[i] = 0u;
 }
 
 // ======================================================= gate GEMM bf16, E <= 16
@@ -188,7 +191,9 @@ __device__ __forceinline__ void rwait4(u32x4& a, u32x4& b, u32x4& c, u32x4& d) {
 __global__ __launch_bounds__(256) void router_skinny_bf16_kernel(const uint16_t* __restrict__ x,
                                                                  const uint16_t* __restrict__ wr,
                                                                  float* __restrict__ dst, int T,
-                                                                 int d, int E, int splits) {
+                                                                 int d, int E, int splits,
+                                                                 uint32_t* __restrict__ clear,
+                                                                 int n_clear) {
   constexpr int P = kSkinnyDepth;
   __shared__ u32x4 tile[4][128];  // per wave: 16 rows x 8 pieces
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -258,6 +263,8 @@ __global__ __launch_bounds__(256) void router_skinny_bf16_kernel(const uint16_t*
       if (e < E) drow[e] = acc[i];
     }
   }
+  if (clear && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+    for (int i = threadIdx.x; i < n_clear; i += 256) clear[i] = 0u;
 }
 
 // Split-K factor: enough blocks to cover the CUs (twice for the skinny kernel,
@@ -285,21 +292,27 @@ int router_splits(const moe_config& c) {
   return (int)s;
 }
 
+// clear != NULL: n_clear words that the kernel sets to zero (the few-token
+// layer's counters).
 hipError_t launch_router_gemm_bf16(const uint16_t* x, const uint16_t* wr, float* dst, int T, int d,
-                                   int E, int splits, hipStream_t st) {
+                                   int E, int splits, hipStream_t st, uint32_t* clear,
+                                   int n_clear) {
   if (E <= 16) {
     router_skinny_bf16_kernel<<<dim3(div_up(T, 64), splits), 256, 0, st>>>(x, wr, dst, T, d, E,
-                                                                           splits);
+                                                                           splits, clear, n_clear);
     return hipGetLastError();
   }
   const int ec = E <= 32 ? 32 : E <= 64 ? 64 : E <= 128 ? 128 : 256;  // E > 16 here
   dim3 grid(div_up(T, 64), splits, div_up(E, ec));
+#define MOE_ROUTER(EC) \
+  router_gemm_bf16_kernel<EC><<<grid, 256, 0, st>>>(x, wr, dst, T, d, E, splits, clear, n_clear)
   switch (ec) {
-    case 32: router_gemm_bf16_kernel<32><<<grid, 256, 0, st>>>(x, wr, dst, T, d, E, splits); break;
-    case 64: router_gemm_bf16_kernel<64><<<grid, 256, 0, st>>>(x, wr, dst, T, d, E, splits); break;
-    case 128: router_gemm_bf16_kernel<128><<<grid, 256, 0, st>>>(x, wr, dst, T, d, E, splits); break;
-    default: router_gemm_bf16_kernel<256><<<grid, 256, 0, st>>>(x, wr, dst, T, d, E, splits); break;
+    case 32: MOE_ROUTER(32); break;
+    case 64: MOE_ROUTER(64); break;
+    case 128: MOE_ROUTER(128); break;
+    default: MOE_ROUTER(256); break;
   }
+#undef MOE_ROUTER
   return hipGetLastError();
 }
 
@@ -325,47 +338,6 @@ hipError_t launch_router_gemm_f32(const float* x, const float* wr, float* dst, i
 }
 
 // ============================================================== top-k + gates
-__device__ __forceinline__ unsigned long long shfl_xor_u64(unsigned long long v, int m) {
-  const int lo = __shfl_xor((int)(uint32_t)v, m);
-  const int hi = __shfl_xor((int)(uint32_t)(v >> 32), m);
-  return ((unsigned long long)(uint32_t)hi << 32) | (uint32_t)lo;
-}
-
-template <int LPT>
-__device__ __forceinline__ unsigned long long seg_max_u64(unsigned long long v) {
-#pragma unroll
-  for (int o = LPT / 2; o > 0; o >>= 1) {
-    const unsigned long long w = shfl_xor_u64(v, o);
-    v = w > v ? w : v;
-  }
-  return v;
-}
-
-template <int LPT>
-__device__ __forceinline__ uint32_t seg_max_u32(uint32_t v) {
-#pragma unroll
-  for (int o = LPT / 2; o > 0; o >>= 1) {
-    const uint32_t w = (uint32_t)__shfl_xor((int)v, o);
-    v = w > v ? w : v;
-  }
-  return v;
-}
-
-template <int LPT>
-__device__ __forceinline__ float seg_sum(float v) {
-#pragma unroll
-  for (int o = LPT / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-
-__device__ __forceinline__ float ord_key_inv(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
-}
-
-constexpr int kMaxEPL = 16;  // E <= 1024 with 64 lanes per token
-
-// EPL: scores per lane (ceil(E / LPT): 1 for E <= 64), so the code holds only
-// the loops a layer of this size needs.
 template <int LPT, int EPL>
 __global__ __launch_bounds__(256) void topk_kernel(const float* __restrict__ partial, int splits,
                                                    const float* __restrict__ bias,
@@ -379,106 +351,13 @@ __global__ __launch_bounds__(256) void topk_kernel(const float* __restrict__ par
   const int q = lane % LPT;
   const int t = (blockIdx.x * 4 + wave) * TPW + lane / LPT;
   const bool live = t < T;
-  const int epl = (E + LPT - 1) / LPT;
-
-  // scores s = z + b (one fp32 add), -0 -> +0; key32 = order-preserving bits
-  uint32_t key[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    key[i] = 0u;
-    const int e = q + i * LPT;
-    if (i < epl && e < E && live) {
-      // every partial is loaded before the first add (one memory latency),
-      // then summed in split order
-      float pv[kMaxSplits];
-#pragma unroll
-      for (int s = 0; s < kMaxSplits; ++s)
-        pv[s] = s < splits ? partial[((size_t)s * T + t) * E + e] : 0.f;
-      float z = pv[0];
-#pragma unroll
-      for (int s = 1; s < kMaxSplits; ++s)
-        if (s < splits) z += pv[s];
-      if (logits_out) logits_out[(size_t)t * E + e] = z;
-      float sc = bias ? __fadd_rn(z, bias[e]) : z;
-      uint32_t u = __float_as_uint(sc);
-      if (u == 0x80000000u) u = 0u;
-      key[i] = ord_key(__uint_as_float(u));
-    }
-  }
-
-  // group-limited eligibility: keep the topk_group groups with the largest max
-  unsigned long long kept = ~0ull;
-  const bool grouped = n_group > 1 && topk_group < n_group;
-  int gsz = E / n_group;
-  if (grouped) {
-    uint32_t my_g = 0u;
-    for (int g = 0; g < n_group; ++g) {
-      uint32_t m = 0u;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = q + i * LPT;
-        if (i < epl && e < E && e / gsz == g) m = key[i] > m ? key[i] : m;
-      }
-      m = seg_max_u32<LPT>(m);
-      if (q == g) my_g = m;
-    }
-    kept = 0ull;
-    for (int r = 0; r < topk_group; ++r) {
-      unsigned long long cand = 0ull;
-      if (q < n_group && !((kept >> q) & 1ull))
-        cand = ((unsigned long long)my_g << 32) | (0xffffffffu - (uint32_t)q);
-      cand = seg_max_u64<LPT>(cand);
-      const int gw = (int)(0xffffffffu - (uint32_t)cand);
-      kept |= 1ull << gw;
-    }
-  }
-
-  // selection rounds: the r-th winner is kept by lane q == r
-  const int nsel = presel > k ? presel : k;
-  uint32_t taken = 0u;
-  int my_e = 0;
-  float my_s = 0.f, s_max = 0.f;
-  for (int r = 0; r < nsel; ++r) {
-    unsigned long long best = 0ull;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = q + i * LPT;
-      const bool ok = i < epl && e < E && !((taken >> i) & 1u) &&
-                      (!grouped || ((kept >> (e / gsz)) & 1ull));
-      const unsigned long long cand =
-          ok ? (((unsigned long long)key[i] << 32) | (0xffffffffu - (uint32_t)e)) : 0ull;
-      best = cand > best ? cand : best;
-    }
-    best = seg_max_u64<LPT>(best);
-    const int we = (int)(0xffffffffu - (uint32_t)best);
-    const float ws = ord_key_inv((uint32_t)(best >> 32));
-    if (we % LPT == q) taken |= 1u << (we / LPT);
-    if (r == 0) s_max = ws;
-    if (q == r) {
-      my_e = we;
-      my_s = ws;
-    }
-  }
-
-  // gates: e_j = exp(s_j - m) over the chosen / pre-selected / all experts
-  const float ej = q < nsel ? expf(my_s - s_max) : 0.f;
-  float denom;
-  if (renorm) {
-    denom = seg_sum<LPT>(q < k ? ej : 0.f);
-  } else if (presel) {
-    denom = seg_sum<LPT>(q < presel ? ej : 0.f);
-  } else {
-    float part = 0.f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = q + i * LPT;
-      if (i < epl && e < E) part += expf(ord_key_inv(key[i]) - s_max);
-    }
-    denom = seg_sum<LPT>(part);
-  }
+  int e;
+  float w;
+  select_token<LPT, EPL>(partial, splits, bias, logits_out, t, live, q, T, E, k, n_group,
+                         topk_group, presel, renorm, &e, &w);
   if (live && q < k) {
-    topk_idx[(size_t)t * k + q] = my_e;
-    topk_w[(size_t)t * k + q] = ej / denom;
+    topk_idx[(size_t)t * k + q] = e;
+    topk_w[(size_t)t * k + q] = w;
   }
 }
 
