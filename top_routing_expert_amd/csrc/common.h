@@ -50,8 +50,7 @@ inline int div_up(long a, long b) { return (int)((a + b - 1) / b); }
 // Every launcher returns hipSuccess or the launch error; shapes are validated
 // by the C-ABI layer before these are called.
 hipError_t launch_router_gemm_bf16(const uint16_t* x, const uint16_t* wr, float* dst, int T, int d,
-                                   int E, int splits, hipStream_t st, uint32_t* clear = nullptr,
-                                   int n_clear = 0);
+                                   int E, int splits, hipStream_t st);
 hipError_t launch_router_gemm_f32(const float* x, const float* wr, float* dst, int T, int d, int E,
                                   hipStream_t st);
 hipError_t launch_topk(const moe_config& c, const float* partial, int splits, const float* bias,

@@ -36,9 +36,7 @@ template <int EC>
 __global__ __launch_bounds__(256) void router_gemm_bf16_kernel(const uint16_t* __restrict__ x,
                                                                const uint16_t* __restrict__ wr,
                                                                float* __restrict__ dst, int T, int d,
-                                                               int E, int splits,
-                                                               uint32_t* __restrict__ clear,
-                                                               int n_clear) {
+                                                               int E, int splits) {
   constexpr int NF = EC / 16;                         // expert fragments per wave
   constexpr int WLOADS = (EC * 8 + 255) / 256;        // 16-byte pieces per thread per chunk
   __shared__ u32x4 sW[2][EC * 8];
@@ -134,8 +132,6 @@ __global__ __launch_bounds__(256) void router_gemm_bf16_kernel(const uint16_t* _
       }
     }
   }
-  if (clear && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
-    for (int i = threadIdx.x; i < n_clear; i += 256) clear[i] = 0u;
 }
 
 // ======================================================= gate GEMM bf16, E <= 16
@@ -191,9 +187,7 @@ __device__ __forceinline__ void rwait4(u32x4& a, u32x4& b, u32x4& c, u32x4& d) {
 __global__ __launch_bounds__(256) void router_skinny_bf16_kernel(const uint16_t* __restrict__ x,
                                                                  const uint16_t* __restrict__ wr,
                                                                  float* __restrict__ dst, int T,
-                                                                 int d, int E, int splits,
-                                                                 uint32_t* __restrict__ clear,
-                                                                 int n_clear) {
+                                                                 int d, int E, int splits) {
   constexpr int P = kSkinnyDepth;
   __shared__ u32x4 tile[4][128];  // per wave: 16 rows x 8 pieces
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -263,8 +257,6 @@ __global__ __launch_bounds__(256) void router_skinny_bf16_kernel(const uint16_t*
       if (e < E) drow[e] = acc[i];
     }
   }
-  if (clear && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
-    for (int i = threadIdx.x; i < n_clear; i += 256) clear[i] = 0u;
 }
 
 // Split-K factor: enough blocks to cover the CUs (twice for the skinny kernel,
@@ -292,27 +284,21 @@ int router_splits(const moe_config& c) {
   return (int)s;
 }
 
-// clear != NULL: n_clear words that the kernel sets to zero (the few-token
-// layer's counters).
 hipError_t launch_router_gemm_bf16(const uint16_t* x, const uint16_t* wr, float* dst, int T, int d,
-                                   int E, int splits, hipStream_t st, uint32_t* clear,
-                                   int n_clear) {
+                                   int E, int splits, hipStream_t st) {
   if (E <= 16) {
     router_skinny_bf16_kernel<<<dim3(div_up(T, 64), splits), 256, 0, st>>>(x, wr, dst, T, d, E,
-                                                                           splits, clear, n_clear);
+                                                                           splits);
     return hipGetLastError();
   }
   const int ec = E <= 32 ? 32 : E <= 64 ? 64 : E <= 128 ? 128 : 256;  // E > 16 here
   dim3 grid(div_up(T, 64), splits, div_up(E, ec));
-#define MOE_ROUTER(EC) \
-  router_gemm_bf16_kernel<EC><<<grid, 256, 0, st>>>(x, wr, dst, T, d, E, splits, clear, n_clear)
   switch (ec) {
-    case 32: MOE_ROUTER(32); break;
-    case 64: MOE_ROUTER(64); break;
-    case 128: MOE_ROUTER(128); break;
-    default: MOE_ROUTER(256); break;
+    case 32: router_gemm_bf16_kernel<32><<<grid, 256, 0, st>>>(x, wr, dst, T, d, E, splits); break;
+    case 64: router_gemm_bf16_kernel<64><<<grid, 256, 0, st>>>(x, wr, dst, T, d, E, splits); break;
+    case 128: router_gemm_bf16_kernel<128><<<grid, 256, 0, st>>>(x, wr, dst, T, d, E, splits); break;
+    default: router_gemm_bf16_kernel<256><<<grid, 256, 0, st>>>(x, wr, dst, T, d, E, splits); break;
   }
-#undef MOE_ROUTER
   return hipGetLastError();
 }
 
@@ -353,8 +339,12 @@ __global__ __launch_bounds__(256) void topk_kernel(const float* __restrict__ par
   const bool live = t < T;
   int e;
   float w;
-  select_token<LPT, EPL>(partial, splits, bias, logits_out, t, live, q, T, E, k, n_group,
-                         topk_group, presel, renorm, &e, &w);
+  auto logit = [&](int i) {
+    const float z = sum_partials(partial, splits, (size_t)T * E, (size_t)t * E + i);
+    if (logits_out) logits_out[(size_t)t * E + i] = z;
+    return z;
+  };
+  select_token<LPT, EPL>(logit, bias, live, q, E, k, n_group, topk_group, presel, renorm, &e, &w);
   if (live && q < k) {
     topk_idx[(size_t)t * k + q] = e;
     topk_w[(size_t)t * k + q] = w;

@@ -8,28 +8,28 @@ namespace moe {
 
 constexpr int kMaxSplits = 16;  // split-K partials of the router GEMM (summed by top-k)
 
-__device__ __forceinline__ unsigned long long shfl_xor_u64(unsigned long long v, int m) {
-  const int lo = __shfl_xor((int)(uint32_t)v, m);
-  const int hi = __shfl_xor((int)(uint32_t)(v >> 32), m);
-  return ((unsigned long long)(uint32_t)hi << 32) | (uint32_t)lo;
+// Maximum over each segment of LPT lanes, in every lane of it: moves within 16
+// lanes (quad permutes, mirrors), then swaps of 16- and 32-lane halves.  A
+// shuffle through LDS instead takes several times as long a step, and the
+// selection rounds are one chain of these.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  const uint32_t w = (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
+  return w > v ? w : v;
 }
-
-template <int LPT>
-__device__ __forceinline__ unsigned long long seg_max_u64(unsigned long long v) {
-#pragma unroll
-  for (int o = LPT / 2; o > 0; o >>= 1) {
-    const unsigned long long w = shfl_xor_u64(v, o);
-    v = w > v ? w : v;
-  }
-  return v;
-}
-
 template <int LPT>
 __device__ __forceinline__ uint32_t seg_max_u32(uint32_t v) {
-#pragma unroll
-  for (int o = LPT / 2; o > 0; o >>= 1) {
-    const uint32_t w = (uint32_t)__shfl_xor((int)v, o);
-    v = w > v ? w : v;
+  if constexpr (LPT >= 2) v = dpp_max<0xB1>(v);    // lanes 1 0 3 2 of a quad
+  if constexpr (LPT >= 4) v = dpp_max<0x4E>(v);    // lanes 2 3 0 1 of a quad
+  if constexpr (LPT >= 8) v = dpp_max<0x141>(v);   // mirrored within 8
+  if constexpr (LPT >= 16) v = dpp_max<0x140>(v);  // mirrored within 16
+  if constexpr (LPT >= 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = p[0] > p[1] ? p[0] : p[1];
+  }
+  if constexpr (LPT >= 64) {
+    const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = p[0] > p[1] ? p[0] : p[1];
   }
   return v;
 }
@@ -47,91 +47,105 @@ __device__ __forceinline__ float ord_key_inv(uint32_t k) {
 
 constexpr int kMaxEPL = 16;  // E <= 1024 with 64 lanes per token
 
-// Lane q = lane % LPT of the group's token t (`live`: t < T; a group without a
-// token runs along).  EPL: scores per lane (ceil(E / LPT): 1 for E <= 64), so
-// the code holds only the loops a layer of this size needs.  The j-th best
-// expert and its gate end up in lane q == j of the group (*out_e, *out_w).
-template <int LPT, int EPL>
-__device__ __forceinline__ void select_token(const float* __restrict__ partial, int splits,
-                                             const float* __restrict__ bias,
-                                             float* __restrict__ logits_out, int t, bool live,
-                                             int q, int T, int E, int k, int n_group,
+// Sum of the router's partial logits of one expert, in split order; every
+// partial is loaded before the first add (one memory latency).
+__device__ __forceinline__ float sum_partials(const float* __restrict__ partial, int splits,
+                                              size_t stride, size_t at) {
+  float pv[kMaxSplits];
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s) pv[s] = s < splits ? partial[s * stride + at] : 0.f;
+  float z = pv[0];
+#pragma unroll
+  for (int s = 1; s < kMaxSplits; ++s)
+    if (s < splits) z += pv[s];
+  return z;
+}
+
+// Lane q = lane % LPT of a token's group (`live`: there is a token; a group
+// without one runs along); logit(e) gives its logits.  EPL: scores per lane
+// (ceil(E / LPT): 1 for E <= 64), so the code holds only the loops a layer of this
+// size needs.  The j-th best expert and its gate end up in lane q == j of the
+// group (*out_e, *out_w).
+template <int LPT, int EPL, typename Logit>
+__device__ __forceinline__ void select_token(Logit&& logit, const float* __restrict__ bias,
+                                             bool live, int q, int E, int k, int n_group,
                                              int topk_group, int presel, int renorm, int* out_e,
                                              float* out_w) {
   const int epl = (E + LPT - 1) / LPT;
 
-  // scores s = z + b (one fp32 add), -0 -> +0; key32 = order-preserving bits
+  // scores s = z + b (one fp32 add), -0 -> +0; key32 = order-preserving bits, at
+  // least 1 (0: no candidate; only a NaN pattern would have it)
   uint32_t key[EPL];
+  uint32_t open = 0u;  // bit i: expert q + i LPT may still be chosen
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     key[i] = 0u;
     const int e = q + i * LPT;
+    if (i < epl && e < E) open |= 1u << i;
     if (i < epl && e < E && live) {
-      // every partial is loaded before the first add (one memory latency),
-      // then summed in split order
-      float pv[kMaxSplits];
-#pragma unroll
-      for (int s = 0; s < kMaxSplits; ++s)
-        pv[s] = s < splits ? partial[((size_t)s * T + t) * E + e] : 0.f;
-      float z = pv[0];
-#pragma unroll
-      for (int s = 1; s < kMaxSplits; ++s)
-        if (s < splits) z += pv[s];
-      if (logits_out) logits_out[(size_t)t * E + e] = z;
+      const float z = logit(e);
       float sc = bias ? __fadd_rn(z, bias[e]) : z;
       uint32_t u = __float_as_uint(sc);
       if (u == 0x80000000u) u = 0u;
-      key[i] = ord_key(__uint_as_float(u));
+      key[i] = max(ord_key(__uint_as_float(u)), 1u);
     }
   }
 
   // group-limited eligibility: keep the topk_group groups with the largest max
-  unsigned long long kept = ~0ull;
-  const bool grouped = n_group > 1 && topk_group < n_group;
-  int gsz = E / n_group;
-  if (grouped) {
-    uint32_t my_g = 0u;
+  if (n_group > 1 && topk_group < n_group) {
+    // e / gsz by a multiplication: exact for e, gsz <= 1024 (1023^2 < 2^20)
+    const uint32_t gsz = E / n_group, inv = ((1u << 20) + gsz - 1) / gsz;
+    int grp[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) grp[i] = (int)((uint32_t)(q + i * LPT) * inv >> 20);
+    uint32_t my_g = 0u;  // lane g: the maximum of group g
     for (int g = 0; g < n_group; ++g) {
       uint32_t m = 0u;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = q + i * LPT;
-        if (i < epl && e < E && e / gsz == g) m = key[i] > m ? key[i] : m;
-      }
+      for (int i = 0; i < EPL; ++i)
+        if (grp[i] == g) m = max(m, key[i]);
       m = seg_max_u32<LPT>(m);
       if (q == g) my_g = m;
     }
-    kept = 0ull;
+    unsigned long long kept = 0ull;
     for (int r = 0; r < topk_group; ++r) {
-      unsigned long long cand = 0ull;
-      if (q < n_group && !((kept >> q) & 1ull))
-        cand = ((unsigned long long)my_g << 32) | (0xffffffffu - (uint32_t)q);
-      cand = seg_max_u64<LPT>(cand);
-      const int gw = (int)(0xffffffffu - (uint32_t)cand);
-      kept |= 1ull << gw;
+      // the best open group, the lowest of equal ones
+      const bool left = q < n_group && !((kept >> q) & 1ull);
+      const uint32_t m = seg_max_u32<LPT>(left ? my_g : 0u);
+      const uint32_t gw = ~seg_max_u32<LPT>(left && my_g == m ? ~(uint32_t)q : 0u);
+      kept |= 1ull << (gw & 63u);
     }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (!((kept >> (grp[i] & 63)) & 1ull)) open &= ~(1u << i);
   }
 
   // selection rounds: the r-th winner is kept by lane q == r
   const int nsel = presel > k ? presel : k;
-  uint32_t taken = 0u;
   int my_e = 0;
   float my_s = 0.f, s_max = 0.f;
   for (int r = 0; r < nsel; ++r) {
-    unsigned long long best = 0ull;
+    // the best open score of this lane, then of the group; the lowest expert of
+    // equal ones
+    uint32_t best = 0u;
+    int mine = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = q + i * LPT;
-      const bool ok = i < epl && e < E && !((taken >> i) & 1u) &&
-                      (!grouped || ((kept >> (e / gsz)) & 1ull));
-      const unsigned long long cand =
-          ok ? (((unsigned long long)key[i] << 32) | (0xffffffffu - (uint32_t)e)) : 0ull;
-      best = cand > best ? cand : best;
+      if (((open >> i) & 1u) && key[i] > best) {
+        best = key[i];
+        mine = q + i * LPT;
+      }
     }
-    best = seg_max_u64<LPT>(best);
-    const int we = (int)(0xffffffffu - (uint32_t)best);
-    const float ws = ord_key_inv((uint32_t)(best >> 32));
-    if (we % LPT == q) taken |= 1u << (we / LPT);
+    const uint32_t m = seg_max_u32<LPT>(best);
+    int we;
+    if constexpr (LPT == 64 && EPL == 1) {  // lane = expert: the first lane that has it
+      we = __ffsll(__ballot(best == m && m > 0u)) - 1;
+      we = max(we, 0);
+    } else {
+      we = min((int)~seg_max_u32<LPT>(best == m && m > 0u ? ~(uint32_t)mine : 0x80000000u), E - 1);
+    }
+    const float ws = ord_key_inv(m);
+    if (we % LPT == q) open &= ~(1u << (we / LPT));
     if (r == 0) s_max = ws;
     if (q == r) {
       my_e = we;
