@@ -159,9 +159,17 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# The current device's index and stream handle without building Stream objects: a
+# decode step's kernels take as long as the calls that launch them.
+_cur_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        torch.cuda.init()
+        return _raw_stream(_cur_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -73,32 +73,47 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const u32x4* __restric
   }
 }
 
-// Row p of x_perm from the codes of token src_of[p] / k (clamped), or of row p.
+// Row p of x_perm from the codes of token src_of[p] / k (clamped), or of row p; U
+// groups of 8 elements a thread, their loads in flight together.
+template <bool BF16, int U>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(
     const uint32_t* __restrict__ codes, const int32_t* __restrict__ src_of,
-    const uint8_t* __restrict__ scales, int k, int T, int row_groups, long groups,
-    u32x4* __restrict__ out_bf16, float* __restrict__ out_f32) {
-  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < groups; i += (long)gridDim.x * 256) {
-    const int p = (int)(i / row_groups), c = (int)(i - (long)p * row_groups);
-    const int t = src_of ? min(max(src_of[p] / k, 0), T - 1) : p;
-    const long g = (long)t * row_groups + c;
-    const uint32_t q = codes[g];
-    const float s = mx_scale(scales[g >> 2]);
-    if (out_bf16) {
+    const uint8_t* __restrict__ scales, int k, int T, uint32_t row_groups, uint32_t groups,
+    u32x4* __restrict__ out) {
+  // 32-bit indexes: T k d < 2^31 elements
+  const uint32_t base = blockIdx.x * (256 * U) + threadIdx.x;
+  uint32_t from[U], q[U];
+  float s[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = min(base + 256 * u, groups - 1);
+    const uint32_t p = i / row_groups, c = i - p * row_groups;
+    const uint32_t t = src_of ? min(max(src_of[p] / k, 0), T - 1) : p;
+    from[u] = t * row_groups + c;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) q[u] = codes[from[u]];
+#pragma unroll
+  for (int u = 0; u < U; ++u) s[u] = mx_scale(scales[from[u] >> 2]);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = base + 256 * u;
+    if (i >= groups) break;
+    if constexpr (BF16) {
       u32x4 o;
-      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0));
-      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1));
-      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 2));
-      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 3));
-      out_bf16[i] = o;
+      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[u], s[u], 0));
+      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[u], s[u], 1));
+      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[u], s[u], 2));
+      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[u], s[u], 3));
+      out[i] = o;
     } else {
-      float4* o = reinterpret_cast<float4*>(out_f32 + 8 * i);
-      const auto v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 0);
-      const auto v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 1);
-      const auto v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 2);
-      const auto v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 3);
-      o[0] = make_float4(v0[0], v0[1], v1[0], v1[1]);
-      o[1] = make_float4(v2[0], v2[1], v3[0], v3[1]);
+      f32x4* o = reinterpret_cast<f32x4*>(out) + 2 * (size_t)i;
+      const auto v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s[u], 0);
+      const auto v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s[u], 1);
+      const auto v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s[u], 2);
+      const auto v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s[u], 3);
+      o[0] = f32x4{v0[0], v0[1], v1[0], v1[1]};
+      o[1] = f32x4{v2[0], v2[1], v3[0], v3[1]};
     }
   }
 }
@@ -124,11 +139,17 @@ hipError_t launch_mx_dequantize(const moe_config& c, const void* codes, const in
                                 const void* scales, void* x_perm, hipStream_t st) {
   const long rows = src_of ? (long)c.T * c.k : c.T;
   const long groups = rows * (c.d / 8);
-  const bool bf = c.dtype == MOE_BF16;
-  mx_dequantize_kernel<<<div_up(groups, 256), 256, 0, st>>>(
-      static_cast<const uint32_t*>(codes), src_of, static_cast<const uint8_t*>(scales), c.k, c.T,
-      c.d / 8, groups, bf ? static_cast<u32x4*>(x_perm) : nullptr,
-      bf ? nullptr : static_cast<float*>(x_perm));
+  constexpr int U = 4;
+  const int blocks = div_up(groups, 256 * U);
+  const auto* cv = static_cast<const uint32_t*>(codes);
+  const auto* sv = static_cast<const uint8_t*>(scales);
+  auto* ov = static_cast<u32x4*>(x_perm);
+  if (c.dtype == MOE_BF16)
+    mx_dequantize_kernel<true, U><<<blocks, 256, 0, st>>>(cv, src_of, sv, c.k, c.T, c.d / 8,
+                                                          (uint32_t)groups, ov);
+  else
+    mx_dequantize_kernel<false, U><<<blocks, 256, 0, st>>>(cv, src_of, sv, c.k, c.T, c.d / 8,
+                                                           (uint32_t)groups, ov);
   return hipGetLastError();
 }
 

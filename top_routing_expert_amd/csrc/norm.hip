@@ -62,10 +62,58 @@ struct Vec16<float> {
   }
 };
 
+// Sum over the wave, the same value in every lane: moves within 16 lanes, then
+// swaps of 16- and 32-lane halves (a shuffle through LDS takes several times as
+// long a step).
+template <int CTRL>
+__device__ __forceinline__ float norm_dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+      (int)__float_as_uint(v), (int)__float_as_uint(v), CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float norm_add_halves(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t w = __float_as_uint(__uint_as_float(p[0]) + __uint_as_float(p[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+// Keeps the compiler from carrying what was computed from v across this point.
+__device__ __forceinline__ void norm_opaque(u32x4& v) { asm volatile("" : "+v"(v)); }
 __device__ __forceinline__ float norm_wave_sum(float v) {
+  v += norm_dpp<0xB1>(v);   // lanes 1 0 3 2 of a quad
+  v += norm_dpp<0x4E>(v);   // lanes 2 3 0 1 of a quad
+  v += norm_dpp<0x141>(v);  // mirrored within 8
+  v += norm_dpp<0x140>(v);  // mirrored within 16
+  return norm_add_halves(v);
+}
+// Wave sums of N values (1, 2, 4, 8 or 16): value j ends up in the lanes whose low bits
+// are j.  Every halving step sends one half of the values and keeps the other, so
+// N values take N - 1 moves and then one chain instead of N chains.
+template <int N>
+__device__ __forceinline__ float norm_wave_sums(const float (&v)[N]) {
+  const int lane = threadIdx.x & 63;
+  float r[N];
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  for (int j = 0; j < N; ++j) r[j] = v[j];
+#pragma unroll
+  for (int bit = 1; bit < N; bit <<= 1) {
+    // r[j], j = 0 .. N / bit - 1: value (j bit + the lane's bits below); keep those with the
+    // next bit as in the lane
+#pragma unroll
+    for (int j = 0; j < N / bit; j += 2) {
+      const bool up = lane & bit;
+      const float keep = up ? r[j + 1] : r[j], send = up ? r[j] : r[j + 1];
+      const float got = bit == 1   ? norm_dpp<0xB1>(send)
+                        : bit == 2 ? norm_dpp<0x4E>(send)
+                                   : __shfl_xor(send, bit);
+      r[j / 2] = keep + got;
+    }
+  }
+  float s = r[0];
+#pragma unroll
+  for (int o = N; o < 16; o <<= 1)
+    s += o == 1 ? norm_dpp<0xB1>(s) : o == 2 ? norm_dpp<0x4E>(s) : __shfl_xor(s, o);
+  return norm_add_halves(s);
 }
 
 // Sum over the block in wave order, the same value for every thread.  `part`
@@ -132,8 +180,9 @@ __global__ __launch_bounds__(MAXT) void norm_fwd_kernel(const u32x4* __restrict_
 
 // Block b: tokens [b per, b per + per) of T, in order; the block's partial
 // weight gradient goes to partial[b].  d_residual NULL: no residual term.
-// Loads of the next token are issued before the current one's sum, so that
-// the barrier hides behind them.
+// The next token's rows are loaded while the current one is summed; what the
+// sum's two sides share is rebuilt from the rows instead of kept, which holds the
+// registers to five waves a SIMD.
 template <typename T, int VPT, int MAXT>
 __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(
     const u32x4* __restrict__ d_xn, const u32x4* __restrict__ x, const u32x4* __restrict__ w,
@@ -143,7 +192,7 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(
   constexpr int N = V::N;
   __shared__ float part[2][kNormMaxThreads / 64];
   const int t0 = blockIdx.x * per, t1 = min(t0 + per, T_);
-  u32x4 wv[VPT], xv[VPT], gv[VPT];
+  u32x4 wv[VPT];
   float S[VPT][N];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -152,56 +201,76 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(
 #pragma unroll
     for (int q = 0; q < N; ++q) S[i][q] = 0.f;
   }
-  auto load = [&](int t) {
+  struct Rows {
+    u32x4 x[VPT], g[VPT], res[VPT];
+    float r;
+  };
+  auto load = [&](int t, Rows& R) {
+    R.r = rstd[t];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + blockDim.x * i;
-      if (v < nvec) {
-        xv[i] = x[(size_t)t * nvec + v];
-        gv[i] = d_xn[(size_t)t * nvec + v];
-      }
+      const int v = min((int)(threadIdx.x + blockDim.x * i), nvec - 1);  // past the row: its end
+      const size_t at = (size_t)t * nvec + v;
+      R.x[i] = __builtin_nontemporal_load(x + at);
+      R.g[i] = __builtin_nontemporal_load(d_xn + at);
+      if (d_residual) R.res[i] = d_residual[at];
     }
   };
-  load(t0);
-  for (int t = t0; t < t1; ++t) {
-    const float r = rstd[t];
-    float n[VPT][N], gw[VPT][N];
-    u32x4 res[VPT];
+  // n and the gradient at it, of vector i
+  auto terms = [&](const Rows& R, int i, float* n, float* gw, float* g) {
+    V::unpack(R.x[i], n);
+    V::unpack(R.g[i], g);
+    float wf[N];
+    if (w) V::unpack(wv[i], wf);
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      n[q] *= R.r;
+      gw[q] = w ? g[q] * wf[q] : g[q];
+    }
+  };
+  auto step = [&](int t, Rows& R, Rows& next) {
+    if (t + 1 < t1) load(t + 1, next);
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + blockDim.x * i;
       if (v < nvec) {
-        if (d_residual) res[i] = d_residual[(size_t)t * nvec + v];
-        float g[N], wf[N];
-        V::unpack(xv[i], n[i]);
-        V::unpack(gv[i], g);
-        if (w) V::unpack(wv[i], wf);
+        float n[N], gw[N], g[N];
+        terms(R, i, n, gw, g);
 #pragma unroll
         for (int q = 0; q < N; ++q) {
-          n[i][q] *= r;
-          S[i][q] = fmaf(g[q], n[i][q], S[i][q]);
-          gw[i][q] = w ? g[q] * wf[q] : g[q];
-          dot = fmaf(gw[i][q], n[i][q], dot);
+          S[i][q] = fmaf(g[q], n[q], S[i][q]);
+          dot = fmaf(gw[q], n[q], dot);
         }
       }
     }
-    if (t + 1 < t1) load(t + 1);
     const float c = norm_block_sum(dot, part[t & 1]) * inv_d;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      norm_opaque(R.x[i]);
+      norm_opaque(R.g[i]);
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + blockDim.x * i;
       if (v < nvec) {
-        float f[N], o[N];
-        if (d_residual) V::unpack(res[i], f);
+        float n[N], gw[N], g[N], f[N], o[N];
+        terms(R, i, n, gw, g);
+        if (d_residual) V::unpack(R.res[i], f);
 #pragma unroll
         for (int q = 0; q < N; ++q) {
-          const float dx = r * (gw[i][q] - n[i][q] * c);
+          const float dx = R.r * (gw[q] - n[q] * c);
           o[q] = d_residual ? f[q] + dx : dx;
         }
         d_x[(size_t)t * nvec + v] = V::pack(o);
       }
     }
+  };
+  Rows A, B;
+  load(t0, A);
+  for (int t = t0; t < t1; t += 2) {
+    step(t, A, B);
+    if (t + 1 < t1) step(t + 1, B, A);
   }
   if (partial) {
 #pragma unroll
@@ -344,7 +413,22 @@ __global__ __launch_bounds__(MAXT) void combine_norm_bwd_kernel(
     const int q_gate = gate ? t / per_gate : 0;
     const u32x4* grow = gate ? gate + (size_t)q_gate * nvec : nullptr;
     u32x4 row[HOLD ? VPT : 1][KC], dv[VPT];
-    float n[VPT][N], dn[VPT][N];
+    float n[VPT][N];
+    // the gradient at n, of vector i
+    auto upstream = [&](int i, int v, float* dn) {
+      float f[N];
+      V::unpack(dv[i], dn);
+      if (w) {
+        V::unpack(w[v], f);
+#pragma unroll
+        for (int q = 0; q < N; ++q) dn[q] *= f[q];
+      }
+      if (gate) {
+        V::unpack(grow[v], f);
+#pragma unroll
+        for (int q = 0; q < N; ++q) dn[q] *= f[q];
+      }
+    };
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + blockDim.x * i;
@@ -360,7 +444,7 @@ __global__ __launch_bounds__(MAXT) void combine_norm_bwd_kernel(
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + blockDim.x * i;
 #pragma unroll
-      for (int q = 0; q < N; ++q) n[i][q] = dn[i][q] = 0.f;
+      for (int q = 0; q < N; ++q) n[i][q] = 0.f;
       if (v >= nvec) continue;
       if constexpr (!HOLD) {
 #pragma unroll
@@ -376,28 +460,18 @@ __global__ __launch_bounds__(MAXT) void combine_norm_bwd_kernel(
           for (int q = 0; q < N; ++q) n[i][q] = fmaf(g[j], f[q], n[i][q]);
         }
       }
-      float df[N], o[N], f[N];
+      float df[N], o[N], dn[N];
       V::unpack(dv[i], df);
 #pragma unroll
       for (int q = 0; q < N; ++q) {
         n[i][q] *= r;
         S[i][q] = fmaf(df[q], n[i][q], S[i][q]);
-        dn[i][q] = df[q];
         o[q] = res_scale * df[q];
       }
       if (d_residual) d_residual[(size_t)t * nvec + v] = V::pack(o);
-      if (w) {
-        V::unpack(w[v], f);
+      upstream(i, v, dn);
 #pragma unroll
-        for (int q = 0; q < N; ++q) dn[i][q] *= f[q];
-      }
-      if (gate) {
-        V::unpack(grow[v], f);
-#pragma unroll
-        for (int q = 0; q < N; ++q) dn[i][q] *= f[q];
-      }
-#pragma unroll
-      for (int q = 0; q < N; ++q) dot = fmaf(dn[i][q], n[i][q], dot);
+      for (int q = 0; q < N; ++q) dot = fmaf(dn[q], n[i][q], dot);
     }
     const float c = norm_block_sum(dot, part[t & 1]) * inv_d;
     float dw[KC];
@@ -405,10 +479,20 @@ __global__ __launch_bounds__(MAXT) void combine_norm_bwd_kernel(
     for (int j = 0; j < KC; ++j) dw[j] = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+      norm_opaque(dv[i]);
+      if constexpr (HOLD) {
+#pragma unroll
+        for (int j = 0; j < KC; ++j) norm_opaque(row[i][j]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + blockDim.x * i;
       if (v >= nvec) continue;
+      float dy[N];
+      upstream(i, v, dy);
 #pragma unroll
-      for (int q = 0; q < N; ++q) dn[i][q] = r * (dn[i][q] - n[i][q] * c);  // dy
+      for (int q = 0; q < N; ++q) dy[q] = r * (dy[q] - n[i][q] * c);
       if constexpr (!HOLD) {
         if (d_topk_w) {
 #pragma unroll
@@ -423,25 +507,21 @@ __global__ __launch_bounds__(MAXT) void combine_norm_bwd_kernel(
           if (d_topk_w) V::unpack(row[HOLD ? i : 0][j], f);
 #pragma unroll
           for (int q = 0; q < N; ++q) {
-            if (d_topk_w) dw[j] = fmaf(dn[i][q], f[q], dw[j]);
-            o[q] = g[j] * dn[i][q];
+            if (d_topk_w) dw[j] = fmaf(dy[q], f[q], dw[j]);
+            o[q] = g[j] * dy[q];
           }
           d_y[(size_t)p[j] * nvec + v] = V::pack(o);
         }
       }
     }
     if (d_topk_w) {  // uniform
-#pragma unroll
-      for (int j = 0; j < KC; ++j)
-        if (j < k) {
-          const float s = norm_wave_sum(dw[j]);
-          if (lane == 0) dots[t & 1][wave][j] = s;
-        }
+      const float s = norm_wave_sums<KC>(dw);
+      if (lane < KC) dots[t & 1][wave][lane] = s;
       __syncthreads();
       if ((int)threadIdx.x < k) {
-        float s = dots[t & 1][0][threadIdx.x];
-        for (int i = 1; i < waves; ++i) s += dots[t & 1][i][threadIdx.x];
-        d_topk_w[(size_t)t * k + threadIdx.x] = s;
+        float v = dots[t & 1][0][threadIdx.x];
+        for (int i = 1; i < waves; ++i) v += dots[t & 1][i][threadIdx.x];
+        d_topk_w[(size_t)t * k + threadIdx.x] = v;
       }
     }
     if (partial && (t + 1 == t1 || (gate && (t + 1) / per_gate != q_gate))) {
@@ -463,12 +543,13 @@ __global__ __launch_bounds__(MAXT) void combine_norm_bwd_kernel(
 }
 
 // ------------------------------------------------------ parameter gradients
-// One block per 64 columns, 16 waves.  For every gate row q: S_q = the sum of its
-// pieces, which are partial rows [first + q, last + q] with first and last the
-// blocks of its first and last token.  d_gate[q] = w S_q; d_w = sum_q gate[q] S_q.
-// SPREAD (few gate rows): the waves take the pieces of one gate row in turn
-// and wave 0 adds their sums; else every wave takes whole gate rows.  Both
-// orders are fixed by T, d and n_gate alone.
+// One block per 32 columns (128 bytes of a partial row), 32 groups of 32 lanes.  For
+// every gate row q: S_q = the sum of its pieces, which are partial rows
+// [first + q, last + q] with first and last the blocks of its first and last token.
+// d_gate[q] = w S_q; d_w = sum_q gate[q] S_q.  Up to 32 gate rows are summed at once by
+// 32 / n_gate groups each; more by one group each, in turn.  Every order is fixed by
+// T, d and n_gate.  (Gate rows in turn by the whole block, 64 columns: 11.5 us for
+// T777-d1028 with 7 gate rows.)
 template <typename T>
 __device__ __forceinline__ float norm_scalar(const void* p, size_t i) {
   if constexpr (sizeof(T) == 2)
@@ -477,55 +558,58 @@ __device__ __forceinline__ float norm_scalar(const void* p, size_t i) {
     return static_cast<const float*>(p)[i];
 }
 
-template <typename T, bool SPREAD>
+template <typename T>
 __global__ __launch_bounds__(1024) void norm_param_grad_kernel(
     const float* __restrict__ partial, const void* __restrict__ w, const void* __restrict__ gate,
     float* __restrict__ d_w, float* __restrict__ d_gate, int d, int n_gate, int per_gate,
     int per) {
-  __shared__ float sums[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + lane;
+  constexpr int GR = 32;  // groups
+  __shared__ float sums[GR][32], dws[GR][32];
+  const int group = threadIdx.x >> 5, c = threadIdx.x & 31, col = blockIdx.x * 32 + c;
   const bool live = col < d;
   const float wc = live && w ? norm_scalar<T>(w, col) : 1.f;
+  const int gpq = n_gate < GR ? GR / n_gate : 1;  // groups of a gate row
   float dw = 0.f;
-  const int step = SPREAD ? 1 : 16;
-  for (int q = SPREAD ? 0 : wave; q < n_gate; q += step) {
+  auto finish = [&](int q, float s) {  // gate row q's sum
+    if (live) {
+      if (d_gate) d_gate[(size_t)q * d + col] = wc * s;
+      dw = fmaf(gate ? norm_scalar<T>(gate, (size_t)q * d + col) : 1.f, s, dw);
+    }
+  };
+  float s = 0.f;
+  for (int q = group / gpq; q < n_gate; q += GR) {  // one turn where gpq > 1
     const int first = (int)((long)q * per_gate / per);
     const int last = (int)(((long)(q + 1) * per_gate - 1) / per);
-    float s = 0.f;
+    s = 0.f;
     if (live) {
       constexpr int U = 8;  // loads in flight
-      const int b0 = first + (SPREAD ? wave : 0), bs = SPREAD ? 16 : 1;
-      for (int b = b0; b <= last; b += U * bs) {
+      for (int b = first + group % gpq; b <= last; b += U * gpq) {
         float v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          v[u] = b + u * bs <= last ? partial[(size_t)(b + u * bs + q) * d + col] : 0.f;
+          v[u] = partial[(size_t)(min(b + u * gpq, last) + q) * d + col];
 #pragma unroll
-        for (int u = 0; u < U; ++u) s += v[u];
+        for (int u = 0; u < U; ++u)
+          if (b + u * gpq <= last) s += v[u];
       }
     }
-    if constexpr (SPREAD) {
-      sums[wave][lane] = s;
-      __syncthreads();
-      s = sums[0][lane];
-#pragma unroll
-      for (int i = 1; i < 16; ++i) s += sums[i][lane];
-      __syncthreads();
-    }
-    if (live) {
-      if (d_gate && (!SPREAD || wave == 0)) d_gate[(size_t)q * d + col] = wc * s;
-      dw = fmaf(gate ? norm_scalar<T>(gate, (size_t)q * d + col) : 1.f, s, dw);
-    }
+    if (gpq == 1) finish(q, s);
   }
-  if constexpr (!SPREAD) {
-    sums[wave][lane] = dw;
+  if (gpq > 1) {
+    sums[group][c] = s;
     __syncthreads();
-    dw = sums[0][lane];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) dw += sums[i][lane];
+    if (group < n_gate) {
+      s = sums[group * gpq][c];
+      for (int i = 1; i < gpq; ++i) s += sums[group * gpq + i][c];
+      finish(group, s);
+    }
   }
-  if (d_w && live && wave == 0) d_w[col] = dw;
+  dws[group][c] = dw;
+  __syncthreads();
+  if (d_w && live && group == 0) {
+    for (int i = 1; i < min(n_gate, GR); ++i) dw += dws[i][c];
+    d_w[col] = dw;
+  }
 }
 
 // ------------------------------------------------------------------ launchers
@@ -591,12 +675,8 @@ static hipError_t launch_param_grad(const moe_config& c, const float* partial, c
   const int n = std::max(n_gate, 1), per_gate = c.T / n;
   with_types(c, [&](auto t) {
     using T = decltype(t);
-    if (n < 16)
-      norm_param_grad_kernel<T, true><<<div_up(c.d, 64), 1024, 0, st>>>(
-          partial, w, gate, d_w, d_gate, c.d, n, per_gate, per);
-    else
-      norm_param_grad_kernel<T, false><<<div_up(c.d, 64), 1024, 0, st>>>(
-          partial, w, gate, d_w, d_gate, c.d, n, per_gate, per);
+    norm_param_grad_kernel<T><<<div_up(c.d, 32), 1024, 0, st>>>(partial, w, gate, d_w, d_gate, c.d,
+                                                                 n, per_gate, per);
   });
   return hipGetLastError();
 }
