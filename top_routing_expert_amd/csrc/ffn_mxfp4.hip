@@ -9,11 +9,18 @@
 // register.  Accumulation is float32.
 //
 // Tile: TW packed weight rows x TM token rows of one expert, 128-wide k stages
-// (64 code bytes and one dword of four scales per row) in a ring in LDS, filled by the LDS-DMA
-// load.  The weight image holds 16-row x 128-k chunks of 1 KB in LDS order, so
-// a wave's copy is 1 KB of consecutive bytes; token rows are copied (and
-// gathered through src_of) from row-major codes.  16-byte pieces are swizzled
-// with (row >> 2) & 3, so the fragment reads of 16 lanes spread over the banks.
+// (64 code bytes per row, one dword of four scales) in a ring in LDS, filled by the
+// LDS-DMA load.  The weight image holds 16-row x 128-k chunks of 1 KB in LDS
+// order, so a wave's copy is 1 KB of consecutive bytes; token rows are copied
+// (and gathered through src_of) from row-major codes.  16-byte pieces are
+// swizzled with (row >> 2) & 3, so the fragment reads of 16 lanes spread over
+// the banks.  The token rows' scales, 4 bytes in a line of their own per row and
+// stage, are copied 16 bytes a row for four stages at a time where K allows it.
+//
+// Persistent: a block walks its tiles in rounds as the bf16 kernel's blocks do
+// (neighbours in the tile order run on one XCD at the same time), and starts the
+// copies of its next tile before it stores the current one.
+#include <algorithm>
 #include <type_traits>
 
 #include "mxfp4.h"
@@ -42,94 +49,140 @@ __device__ __forceinline__ void mx_wait_vm_barrier() {
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// GW x GT waves, each WA x WB fragments of 32 weight rows x 32 tokens.
-template <bool GATED, int GW, int GT, int WA, int WB, int STAGES>
+// GW x GT waves, each WA x WB fragments of 32 weight rows x 32 tokens.  S4: token
+// scales by groups of four stages, in a double buffer of their own.
+template <int GW, int GT, int WA, int WB, int STAGES, bool S4>
 struct MxTile {
   static constexpr int NW = GW * GT;
   static constexpr int TW = 32 * GW * WA, TM = 32 * GT * WB;
   static constexpr int ROWS = TW + TM;
-  static constexpr int CODE_CHUNKS = ROWS / 16;          // 1 KB copies per stage
-  static constexpr int CPW = CODE_CHUNKS / NW;           // per wave
-  static constexpr int SCALE_CHUNKS = ROWS / 64;         // 256-byte copies per stage
+  static constexpr int CPW = ROWS / 16 / NW;             // 1 KB code copies per wave and stage
+  static constexpr int SROWS = S4 ? TW : ROWS;           // rows with scales in the ring
+  static constexpr int SCALE_CHUNKS = SROWS / 64;        // 256-byte copies per stage
   static constexpr int SPW = (SCALE_CHUNKS + NW - 1) / NW;
   static constexpr int DPW = CPW + SPW;                  // copies per wave and stage
-  static constexpr int STAGE_BYTES = ROWS * 68;
-  static_assert(CODE_CHUNKS % NW == 0 && ROWS % 64 == 0 && TW % 64 == 0, "stage split");
-  static_assert(STAGES * STAGE_BYTES <= 156 * 1024, "LDS ring too large");
-  static_assert(STAGES >= 3 && STAGES <= 6, "ring depth");
-  static_assert((STAGES - 2) * DPW <= 63, "vmcnt range");
+  static constexpr int STAGE_BYTES = ROWS * 64 + SROWS * 4;
+  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+  static constexpr int GROUP_BYTES = S4 ? TM * 16 : 0;   // token scales of four stages
+  static constexpr int GROUP_CHUNKS = S4 ? TM / 64 : 0;  // 1 KB copies per group
+  static constexpr int GPW = (GROUP_CHUNKS + NW - 1) / NW;
+  static_assert(TW % (16 * NW) == 0 && TM % (16 * NW) == 0 && ROWS % 64 == 0 && TW % 64 == 0 &&
+                    TM % 64 == 0,
+                "stage split");
+  static_assert(RING_BYTES + 2 * GROUP_BYTES + 12 * kTileTableMax + 64 <= 160 * 1024, "LDS");
+  static_assert(STAGES >= 3 && STAGES <= 5, "ring depth");
+  static_assert((STAGES - 1) * DPW + GPW <= 63, "vmcnt range");
 };
 
-template <bool GATED, int GW, int GT, int WA, int WB, int STAGES, int BLOCKS>
+template <bool GATED, int GW, int GT, int WA, int WB, int STAGES, int BLOCKS, bool S4>
 __global__ __launch_bounds__(64 * GW * GT, BLOCKS * GW * GT / 4) void mxfp4_gemm_kernel(
     const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
     const int32_t* __restrict__ src_of, int gk, int gtokens, const int32_t* __restrict__ offs,
     const uint8_t* __restrict__ image, size_t codes_bytes, size_t expert_bytes,
     uint16_t* __restrict__ out, int E, int R, int N, int K, int rows, int n_tiles, int band) {
-  using G = MxTile<GATED, GW, GT, WA, WB, STAGES>;
+  using G = MxTile<GW, GT, WA, WB, STAGES, S4>;
   constexpr int TW = G::TW, TM = G::TM, ROWS = G::ROWS, NW = G::NW;
-  __shared__ __attribute__((aligned(16))) unsigned char ring[STAGES * G::STAGE_BYTES];
-  __shared__ int s_tile[4];
+  __shared__ __attribute__((aligned(16))) unsigned char lds[G::RING_BYTES + 2 * G::GROUP_BYTES];
+  __shared__ int s_o0[kTileTableMax], s_o1[kTileTableMax], s_start[kTileTableMax];
+  __shared__ int s_tile[2][4];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  if (wave == 0) place_tile<TM>(offs, E, rows, n_tiles, band, lane, s_tile);
-  __syncthreads();
-  const int e = __builtin_amdgcn_readfirstlane(s_tile[0]);
-  if (e < 0) return;  // block-uniform
-  const int row0 = __builtin_amdgcn_readfirstlane(s_tile[1]);
-  const int row_end = __builtin_amdgcn_readfirstlane(s_tile[2]);
-  const int n_tile = __builtin_amdgcn_readfirstlane(s_tile[3]);
-  const int pr0 = n_tile * TW;  // first packed row of the tile
   const int nk = K / kMxStepK;  // stages
+  const int grid = (int)gridDim.x;  // a multiple of 8
+  const int qp = (grid >> 3) * (int)(blockIdx.x & 7) + (int)(blockIdx.x >> 3);
+  int total = 0;  // tiles (wave 0 only)
+  // tile of this block in a round, into s_tile[round & 1] (expert -1: none); wave 0
+  auto place = [&](int round) {
+    int* t = s_tile[round & 1];
+    const int L = round * grid + ((round & 1) ? grid - 1 - qp : qp);
+    if (lane == 0) t[0] = -1;
+    if (L < total) locate_in_table<TM>(s_o0, s_o1, s_start, E, n_tiles, band, L, lane, t);
+  };
+  if (wave == 0) {  // the table is written and read by this one wave
+    total = build_tile_table<TM>(offs, E, rows, n_tiles, lane, s_o0, s_o1, s_start);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    place(0);
+  }
+  __syncthreads();
 
   // ---- copies of this wave: code chunks wave + NW i (weight chunks first), then
-  // scale chunks wave + NW i (the last one repeated where they do not come out
-  // even: the same bytes to the same place).  Rows past the expert's last
-  // packed row or token read a real row and feed outputs that are not stored.
-  // Offsets are 32-bit: a weight chunk's base is a 64-bit scalar, T rows of codes
-  // are below 2^31 bytes.
-  auto token_of = [&](int r) {
-    const int p = min(row0 + r, row_end - 1);
-    return src_of ? min(max(src_of[p] / gk, 0), gtokens - 1) : p;
+  // scale chunks wave + NW i, and every fourth stage a chunk of token scales (the
+  // last one repeated where they do not come out even: the same bytes to the same
+  // place).  Rows past the expert's last packed row or token read a real row and
+  // feed outputs that are not stored.  Offsets are 32-bit: a weight chunk's base
+  // is a 64-bit scalar, T rows of codes are below 2^31 bytes.
+  constexpr int WCH = TW / (16 * NW);  // weight chunks of a wave; then token chunks
+  struct Tile {
+    int row0, row_end, pr0;  // token rows, first packed row
   };
-  const uint8_t* we = image + (size_t)e * expert_bytes;
-  const uint8_t* wse = we + codes_bytes;
-  uint32_t voff[G::CPW], soff[G::SPW];
-#pragma unroll
-  for (int i = 0; i < G::CPW; ++i) {
-    const int r = 16 * (wave + NW * i);
-    if (r < TW) {
-      voff[i] = 16u * lane;
-    } else {
-      const int rr = lane >> 2;  // row of the chunk
-      voff[i] = (uint32_t)token_of(r - TW + rr) * (uint32_t)(K / 2) +
-                16u * (uint32_t)((lane & 3) ^ ((rr >> 2) & 3));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < G::SPW; ++i) {
-    const int r = 64 * min(wave + NW * i, G::SCALE_CHUNKS - 1);
-    soff[i] = r < TW ? 4u * lane : (uint32_t)token_of(r - TW + lane) * (uint32_t)(K / 32);
-  }
-  const uint32_t lds0 = (uint32_t)(size_t)(const mx_lds_t*)ring;
-  auto issue = [&](int kt) {
-    const uint32_t sb = lds0 + (uint32_t)(kt % STAGES) * (uint32_t)G::STAGE_BYTES;
+  uint32_t voff[G::CPW], soff[G::SPW], goff[S4 ? G::GPW : 1];
+  const uint8_t* cbase[G::CPW];
+  const uint8_t* sbase[G::SPW];
+  uint32_t sstep[G::SPW];
+  auto open = [&](int round, Tile* t) {
+    const int* st = s_tile[round & 1];
+    const int e = __builtin_amdgcn_readfirstlane(st[0]);
+    if (e < 0) return false;  // block-uniform; later rounds only hold larger tile numbers
+    t->row0 = __builtin_amdgcn_readfirstlane(st[1]);
+    t->row_end = __builtin_amdgcn_readfirstlane(st[2]);
+    t->pr0 = __builtin_amdgcn_readfirstlane(st[3]) * TW;
+    auto token_of = [&](int r) {
+      const int p = min(t->row0 + r, t->row_end - 1);
+      return src_of ? min(max(src_of[p] / gk, 0), gtokens - 1) : p;
+    };
+    const uint8_t* we = image + (size_t)e * expert_bytes;
+    const uint8_t* wse = we + codes_bytes;
 #pragma unroll
     for (int i = 0; i < G::CPW; ++i) {
-      const int c = wave + NW * i;  // wave-uniform
-      const uint8_t* base =
-          16 * c < TW ? we + ((size_t)min(pr0 / 16 + c, R / 16 - 1) * nk + kt) * 1024
-                      : xc + (size_t)kt * 64;
-      mx_dma16(base, voff[i], sb + (uint32_t)c * 1024u);
+      const int c = wave + NW * i;
+      if (i < WCH) {
+        cbase[i] = we + (size_t)min(t->pr0 / 16 + c, R / 16 - 1) * nk * 1024;
+        voff[i] = 16u * lane;
+      } else {
+        const int rr = lane >> 2;  // row of the chunk
+        cbase[i] = xc;
+        voff[i] = (uint32_t)token_of(16 * c - TW + rr) * (uint32_t)(K / 2) +
+                  16u * (uint32_t)((lane & 3) ^ ((rr >> 2) & 3));
+      }
     }
 #pragma unroll
     for (int i = 0; i < G::SPW; ++i) {
       const int c = min(wave + NW * i, G::SCALE_CHUNKS - 1);
-      const uint8_t* base =
-          64 * c < TW ? wse + ((size_t)min(pr0 / 64 + c, R / 64 - 1) * nk + kt) * 256
-                      : xs + (size_t)kt * 4;
-      mx_dma4(base, soff[i], sb + (uint32_t)(ROWS * 64) + (uint32_t)c * 256u);
+      const bool weight = S4 || 64 * c < TW;  // wave-uniform
+      sbase[i] = weight ? wse + (size_t)min(t->pr0 / 64 + c, R / 64 - 1) * nk * 256 : xs;
+      sstep[i] = weight ? 256u : 4u;
+      soff[i] = weight ? 4u * lane : (uint32_t)token_of(64 * c - TW + lane) * (uint32_t)(K / 32);
+    }
+    if constexpr (S4) {
+#pragma unroll
+      for (int i = 0; i < G::GPW; ++i)
+        goff[i] = (uint32_t)token_of(64 * min(wave + NW * i, G::GROUP_CHUNKS - 1) + lane) *
+                  (uint32_t)(K / 32);
+    }
+    return true;
+  };
+  const uint32_t lds0 = (uint32_t)(size_t)(const mx_lds_t*)lds;
+  // `group`: whether stage kt begins a group of token scales
+  auto issue = [&](int kt, bool group) {
+    const uint32_t sb = lds0 + (uint32_t)(kt % STAGES) * (uint32_t)G::STAGE_BYTES;
+#pragma unroll
+    for (int i = 0; i < G::CPW; ++i)
+      mx_dma16(cbase[i] + (size_t)kt * (i < WCH ? 1024 : 64), voff[i],
+               sb + (uint32_t)(wave + NW * i) * 1024u);
+#pragma unroll
+    for (int i = 0; i < G::SPW; ++i)
+      mx_dma4(sbase[i] + (size_t)kt * sstep[i], soff[i],
+              sb + (uint32_t)(ROWS * 64) +
+                  (uint32_t)min(wave + NW * i, G::SCALE_CHUNKS - 1) * 256u);
+    if constexpr (S4) {
+      if (group) {  // one copy more: the waits, which count without it, are early
+#pragma unroll
+        for (int i = 0; i < G::GPW; ++i)
+          mx_dma16(xs + (size_t)kt * 4, goff[i],
+                   lds0 + (uint32_t)G::RING_BYTES + (uint32_t)((kt / 4) & 1) * G::GROUP_BYTES +
+                       (uint32_t)min(wave + NW * i, G::GROUP_CHUNKS - 1) * 1024u);
+      }
     }
   };
 
@@ -138,17 +191,8 @@ __global__ __launch_bounds__(64 * GW * GT, BLOCKS * GW * GT / 4) void mxfp4_gemm
   const int lk = lane >> 5;
   const int arow0 = wn * 32 * WA + (lane & 31);
   const int tok0 = wm * 32 * WB;
-  const int jn =
-      __builtin_amdgcn_readfirstlane(min(WB, max(0, (row_end - row0 - tok0 + 31) >> 5)));
   const int brow0 = TW + tok0 + (lane & 31);
-
   f32x16 acc[WA][WB];
-#pragma unroll
-  for (int i = 0; i < WA; ++i)
-#pragma unroll
-    for (int j = 0; j < WB; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
   auto wait_later = [&](int later) {  // all stages but the `later` youngest are in
     switch (later) {
@@ -156,138 +200,212 @@ __global__ __launch_bounds__(64 * GW * GT, BLOCKS * GW * GT / 4) void mxfp4_gemm
       case 1: mx_wait_vm_barrier<G::DPW>(); break;
       case 2: mx_wait_vm_barrier<2 * G::DPW>(); break;
       case 3: mx_wait_vm_barrier<3 * G::DPW>(); break;
-      default: mx_wait_vm_barrier<4 * G::DPW>(); break;
+      case 4: mx_wait_vm_barrier<4 * G::DPW>(); break;
+      default: mx_wait_vm_barrier<0>(); break;
     }
+  };
+  auto begin = [&] {  // the first stages of a tile
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i)
+      if (i < nk) issue(i, i % 4 == 0);
   };
   auto main_loop = [&](auto jn_c) {
     constexpr int JN = decltype(jn_c)::value;
-    struct Frags {
-      u32x4 a[WA][2], b[WB][2];
-      uint32_t as[WA], bs[WB];
+    struct Half {  // the fragments of one 64-wide step
+      u32x4 a[WA], b[WB];
     };
-    auto load_frags = [&](int kt, Frags& F) {
-      const unsigned char* sb = ring + (kt % STAGES) * G::STAGE_BYTES;
-      auto piece = [&](int row, int q) {
-        return *reinterpret_cast<const u32x4*>(sb + row * 64 + ((q ^ ((row >> 2) & 3)) << 4));
-      };
-      auto scale = [&](int row) {  // this lane's two scales in bytes 0 and 2
-        return *reinterpret_cast<const uint32_t*>(sb + ROWS * 64 + row * 4) >> (8 * lk);
+    struct Scales {  // of a stage, four bytes a row
+      uint32_t a[WA], b[WB];
+    };
+    auto stage_at = [&](int kt) { return lds + (kt % STAGES) * G::STAGE_BYTES; };
+    auto read_half = [&](int kt, int h, Half& F) {
+      const unsigned char* sb = stage_at(kt);
+      auto piece = [&](int row) {
+        return *reinterpret_cast<const u32x4*>(sb + row * 64 +
+                                               (((2 * h + lk) ^ ((row >> 2) & 3)) << 4));
       };
 #pragma unroll
-      for (int i = 0; i < WA; ++i) {
-        F.a[i][0] = piece(arow0 + 32 * i, lk);
-        F.a[i][1] = piece(arow0 + 32 * i, 2 + lk);
-        F.as[i] = scale(arow0 + 32 * i);
-      }
+      for (int i = 0; i < WA; ++i) F.a[i] = piece(arow0 + 32 * i);
 #pragma unroll
-      for (int j = 0; j < JN; ++j) {
-        F.b[j][0] = piece(brow0 + 32 * j, lk);
-        F.b[j][1] = piece(brow0 + 32 * j, 2 + lk);
-        F.bs[j] = scale(brow0 + 32 * j);
-      }
+      for (int j = 0; j < JN; ++j) F.b[j] = piece(brow0 + 32 * j);
+    };
+    auto read_scales = [&](int kt, Scales& S) {
+      const unsigned char* sb = stage_at(kt) + ROWS * 64;
+#pragma unroll
+      for (int i = 0; i < WA; ++i)
+        S.a[i] = *reinterpret_cast<const uint32_t*>(sb + (arow0 + 32 * i) * 4);
+      const unsigned char* tb = S4 ? lds + G::RING_BYTES + ((kt / 4) & 1) * G::GROUP_BYTES +
+                                         (kt % 4) * 4 - TW * 16
+                                   : sb;
+#pragma unroll
+      for (int j = 0; j < JN; ++j)
+        S.b[j] = *reinterpret_cast<const uint32_t*>(tb + (brow0 + 32 * j) * (S4 ? 16 : 4));
     };
     auto wide = [](u32x4 v) -> i32x8 {  // E2M1 operands use the first four registers
       return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
     };
-    auto mfma_stage = [&](const Frags& F) {
+    // a lane's scale of half h is byte 2 h + lk; shifted here and not behind the
+    // read, which would make the reads wait before the MFMAs they hide under
+    auto mfma_half = [&](const Half& F, const Scales& S, auto h_c) {
+      constexpr int H = decltype(h_c)::value;
+      int as[WA], bs[WB];
+#pragma unroll
+      for (int i = 0; i < WA; ++i) as[i] = (int)(S.a[i] >> (8 * lk));
+#pragma unroll
+      for (int j = 0; j < JN; ++j) bs[j] = (int)(S.b[j] >> (8 * lk));
 #pragma unroll
       for (int j = 0; j < JN; ++j)
 #pragma unroll
         for (int i = 0; i < WA; ++i)
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              wide(F.a[i][0]), wide(F.b[j][0]), acc[i][j], 4, 4, 0, (int)F.as[i], 0, (int)F.bs[j]);
-#pragma unroll
-      for (int j = 0; j < JN; ++j)
-#pragma unroll
-        for (int i = 0; i < WA; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              wide(F.a[i][1]), wide(F.b[j][1]), acc[i][j], 4, 4, 2, (int)F.as[i], 2, (int)F.bs[j]);
+              wide(F.a[i]), wide(F.b[j]), acc[i][j], 4, 4, 2 * H, as[i], 2 * H, bs[j]);
     };
-    // Stage kt sits in ring slot kt % STAGES; its fragments are read during
-    // step kt - 1.  End of step kt: wait for this wave's copies of stage kt + 2,
-    // barrier (every wave's copies of kt + 2 are in and nobody reads stage kt any more),
-    // then refill its slot with stage kt + STAGES.
-#pragma unroll
-    for (int i = 0; i < STAGES; ++i)
-      if (i < nk) issue(i);
-    wait_later(max(0, min(nk - 1, STAGES - 1) - 1));  // stages 0 and 1 are in
-    Frags F0, F1;
-    if (JN > 0) load_frags(0, F0);
-    auto step = [&](int kt, Frags& cur, Frags& nxt) {
-      if (JN > 0) {
-        load_frags(min(kt + 1, nk - 1), nxt);  // the last step re-reads its own stage
-        mfma_stage(cur);
-      }
-      if (kt + 2 < nk)
-        wait_later(min(nk - 1, kt + STAGES - 1) - (kt + 2));
-      else
-        mx_wait_vm_barrier<0>();
-      if (kt + STAGES < nk) issue(kt + STAGES);
-    };
-    for (int kt = 0; kt < nk; kt += 2) {
-      step(kt, F0, F1);
-      if (kt + 1 < nk) step(kt + 1, F1, F0);
+    // Stage kt sits in ring slot kt % STAGES.  Step kt: its second half is read
+    // while the first half's MFMAs run; then the wait for stage kt + 1 and the
+    // barrier (every wave's copies of kt + 1 are in and stage kt is in
+    // registers), the refill of the slot with stage kt + STAGES, and the first half
+    // of stage kt + 1 is read while the second half's MFMAs run.  (A token-scale
+    // group's buffer is refilled two groups later.)
+    //
+    // The MFMAs are pinned between the reads they cover and the next wait: they
+    // touch no memory, so the compiler is free to move them behind the barrier, where
+    // nothing would hide under them any more (T8192-E64 gate / up 1304 ->
+    // 1225 us).  Within the unrolled loop, one basic block, the scheduling barriers
+    // do; at the end of a tile the accumulators pass through empty asm.
+    const auto H0 = std::integral_constant<int, 0>();
+    const auto H1 = std::integral_constant<int, 1>();
+    Half P, Q;
+    Scales SA, SB;
+    wait_later(min(nk, STAGES) - 1);  // stage 0 is in
+    if (JN > 0) {
+      read_half(0, 0, P);
+      read_scales(0, SA);
     }
-  };
-  switch (jn) {
-    case 0: main_loop(std::integral_constant<int, 0>()); break;
-    case 1: main_loop(std::integral_constant<int, 1>()); break;
-    case 2: main_loop(std::integral_constant<int, (WB >= 2 ? 2 : WB)>()); break;
-    case 3: main_loop(std::integral_constant<int, (WB >= 3 ? 3 : WB)>()); break;
-    default: main_loop(std::integral_constant<int, WB>()); break;
-  }
-
-  // ---- epilogue: acc[i][j][4 g + r] = C[fragment-i row 8 g + 4 lk + r][token lane & 31]
+    auto step = [&](int kt, int u, const Scales& cur, Scales& nxt, auto full_c) {
+      constexpr bool FULL = decltype(full_c)::value;  // kt + u + STAGES < nk; kt % 4 == 0
+      const int s = kt + u;
+      if (JN > 0) {
+        read_half(s, 1, Q);
+        __builtin_amdgcn_sched_barrier(0);
+        mfma_half(P, cur, H0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!FULL) {
 #pragma unroll
-  for (int j = 0; j < WB; ++j) {
-    const int p = row0 + tok0 + 32 * j + (lane & 31);
-    if (j >= jn || p >= row_end) continue;
+          for (int j = 0; j < JN; ++j)
 #pragma unroll
-    for (int i = 0; i < WA; ++i) {
-      const int prf = pr0 + wn * 32 * WA + 32 * i;  // first packed row of the fragment
-      if (prf >= R) continue;
-      if constexpr (GATED) {  // rows 0..15 gate, 16..31 up of the same 16 features
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float hv[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float a = acc[i][j][4 * g + r], u = acc[i][j][4 * g + 8 + r];
-            hv[r] = a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)) * u;
-          }
-          u32x2 pk;
-          pk.x = pack_bf16x2(hv[0], hv[1]);
-          pk.y = pack_bf16x2(hv[2], hv[3]);
-          *reinterpret_cast<u32x2*>(out + (size_t)p * N + prf / 2 + 8 * g + 4 * lk) = pk;
+            for (int i = 0; i < WA; ++i) asm volatile("" : "+v"(acc[i][j]));
         }
+      }
+      if constexpr (FULL) {
+        mx_wait_vm_barrier<(STAGES - 2) * G::DPW>();
+        issue(s + STAGES, (u + STAGES) % 4 == 0);
       } else {
+        wait_later(max(0, min(nk - 1, s + STAGES - 1) - (s + 1)));
+        if (s + STAGES < nk) issue(s + STAGES, (s + STAGES) % 4 == 0);
+      }
+      if (JN > 0) {
+        const int n = FULL ? s + 1 : min(s + 1, nk - 1);  // past the end: any stage
+        read_half(n, 0, P);
+        read_scales(n, nxt);
+        __builtin_amdgcn_sched_barrier(0);
+        mfma_half(Q, cur, H1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    int kt = 0;
+    for (; kt + 3 + STAGES < nk; kt += 4) {
+      step(kt, 0, SA, SB, std::true_type());
+      step(kt, 1, SB, SA, std::true_type());
+      step(kt, 2, SA, SB, std::true_type());
+      step(kt, 3, SB, SA, std::true_type());
+    }
+    for (; kt < nk; kt += 2) {
+      step(kt, 0, SA, SB, std::false_type());
+      if (kt + 1 < nk) step(kt, 1, SB, SA, std::false_type());
+    }
+    // the last reads are done before the ring is filled for the next tile
+    mx_wait_vm_barrier<0>();
+  };
+
+  Tile cur{};
+  bool more = open(0, &cur);
+  if (more) begin();
+  for (int round = 0; more; ++round) {
+    const int jn =
+        __builtin_amdgcn_readfirstlane(min(WB, max(0, (cur.row_end - cur.row0 - tok0 + 31) >> 5)));
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          u32x2 pk;
-          pk.x = pack_bf16x2(acc[i][j][4 * g], acc[i][j][4 * g + 1]);
-          pk.y = pack_bf16x2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
-          *reinterpret_cast<u32x2*>(out + (size_t)p * N + prf + 8 * g + 4 * lk) = pk;
+    for (int i = 0; i < WA; ++i)
+#pragma unroll
+      for (int j = 0; j < WB; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    if (wave == 0) place(round + 1);  // read after the main loop's barriers
+    switch (jn) {
+      case 0: main_loop(std::integral_constant<int, 0>()); break;
+      case 1: main_loop(std::integral_constant<int, 1>()); break;
+      case 2: main_loop(std::integral_constant<int, (WB >= 2 ? 2 : WB)>()); break;
+      case 3: main_loop(std::integral_constant<int, (WB >= 3 ? 3 : WB)>()); break;
+      default: main_loop(std::integral_constant<int, WB>()); break;
+    }
+    // every wave has read its last fragments and no copy is in flight: the next
+    // tile's copies run under this one's stores
+    const Tile t = cur;
+    more = open(round + 1, &cur);
+    if (more) begin();
+
+    // ---- epilogue: acc[i][j][4 g + r] = C[fragment-i row 8 g + 4 lk + r][token lane & 31]
+#pragma unroll
+    for (int j = 0; j < WB; ++j) {
+      const int p = t.row0 + tok0 + 32 * j + (lane & 31);
+      if (j >= jn || p >= t.row_end) continue;
+#pragma unroll
+      for (int i = 0; i < WA; ++i) {
+        const int prf = t.pr0 + wn * 32 * WA + 32 * i;  // first packed row of the fragment
+        if (prf >= R) continue;
+        if constexpr (GATED) {  // rows 0..15 gate, 16..31 up of the same 16 features
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float hv[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float a = acc[i][j][4 * g + r], u = acc[i][j][4 * g + 8 + r];
+              hv[r] = a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)) * u;
+            }
+            u32x2 pk;
+            pk.x = pack_bf16x2(hv[0], hv[1]);
+            pk.y = pack_bf16x2(hv[2], hv[3]);
+            *reinterpret_cast<u32x2*>(out + (size_t)p * N + prf / 2 + 8 * g + 4 * lk) = pk;
+          }
+        } else {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            u32x2 pk;
+            pk.x = pack_bf16x2(acc[i][j][4 * g], acc[i][j][4 * g + 1]);
+            pk.y = pack_bf16x2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
+            *reinterpret_cast<u32x2*>(out + (size_t)p * N + prf + 8 * g + 4 * lk) = pk;
+          }
         }
       }
     }
   }
 }
 
-template <bool GATED, int GW, int GT, int WA, int WB, int STAGES, int BLOCKS>
+template <bool GATED, int GW, int GT, int WA, int WB, int STAGES, int BLOCKS, bool S4>
 static hipError_t launch_tile(const moe_config& c, const void* codes, const void* scales,
                               const int32_t* src_of, const int32_t* offs, const void* image,
                               void* out, hipStream_t st) {
-  using G = MxTile<GATED, GW, GT, WA, WB, STAGES>;
+  using G = MxTile<GW, GT, WA, WB, STAGES, S4>;
   const MxGeom g = mx_geom(c, GATED);
   const long rows = (long)c.T * c.k;
   const int n_tiles = div_up(g.rows, G::TW);
   const long total = (long)n_tiles * worst_row_tiles(rows, c.E, G::TM);
-  const int blocks = (int)((total + 7) / 8 * 8);
-  mxfp4_gemm_kernel<GATED, GW, GT, WA, WB, STAGES, BLOCKS><<<blocks, 64 * GW * GT, 0, st>>>(
+  const long cap = ((long)BLOCKS * device_cus() + 7) / 8 * 8;
+  const int blocks = (int)std::min(cap, (total + 7) / 8 * 8);
+  mxfp4_gemm_kernel<GATED, GW, GT, WA, WB, STAGES, BLOCKS, S4><<<blocks, 64 * GW * GT, 0, st>>>(
       static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), src_of, c.k, c.T,
       offs, static_cast<const uint8_t*>(image), g.codes_bytes, g.expert_bytes,
-      static_cast<uint16_t*>(out), c.E, (int)g.rows,
-      GATED ? c.f : c.d, GATED ? c.d : c.f, (int)rows, n_tiles, 8);
+      static_cast<uint16_t*>(out), c.E, (int)g.rows, GATED ? c.f : c.d, GATED ? c.d : c.f,
+      (int)rows, n_tiles, 8);
   return hipGetLastError();
 }
 
@@ -296,9 +414,17 @@ static hipError_t launch_mx_gemm(const moe_config& c, const void* codes, const v
                                  const int32_t* src_of, const int32_t* offs, const void* image,
                                  void* out, hipStream_t st) {
   const long rows = (long)c.T * c.k;
-  if (rows >= 128L * c.E)
-    return launch_tile<GATED, 4, 2, 2, 4, 4, 1>(c, codes, scales, src_of, offs, image, out, st);
-  return launch_tile<GATED, 4, 1, 1, 2, 4, 2>(c, codes, scales, src_of, offs, image, out, st);
+  // groups of four stages of token scales: whole groups at 16-byte addresses
+  const bool s4 = (GATED ? c.d : c.f) % 512 == 0 && reinterpret_cast<uintptr_t>(scales) % 16 == 0;
+  if (rows >= 128L * c.E) {
+    if (s4)
+      return launch_tile<GATED, 4, 2, 2, 4, 4, 1, true>(c, codes, scales, src_of, offs, image, out,
+                                                        st);
+    return launch_tile<GATED, 4, 2, 2, 4, 4, 1, false>(c, codes, scales, src_of, offs, image, out,
+                                                       st);
+  }
+  return launch_tile<GATED, 4, 1, 1, 2, 4, 2, false>(c, codes, scales, src_of, offs, image, out,
+                                                     st);
 }
 
 hipError_t launch_ffn_gate_up_mxfp4(const moe_config& c, const void* x_codes, const void* x_scales,
