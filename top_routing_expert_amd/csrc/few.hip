@@ -572,6 +572,10 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_layer_kernel(FewArgs a) {
       if (ready) return;
       if (wave == 0)
         while (!__all(marks(a.done) == every)) __builtin_amdgcn_s_sleep(4);
+      // h by ordinary loads, a row once per XCD (29 tokens, 58 rows of 2816 bytes: 88 -> 78
+      // us); where it is copied to LDS once a block, going around the caches costs less
+      // than emptying them (one token: 30 against 33 us)
+      if (wave == 0 && !h_lds) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
       __syncthreads();
       if (h_lds) {
         const int nv = a.f / 8;
@@ -611,14 +615,14 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_layer_kernel(FewArgs a) {
     } else {
       const u32x4* hv = reinterpret_cast<const u32x4*>(a.h);
       using Step = FewStep<MX, 1, true>;
-      few_stream<MX ? 2 : 5, Step>(
+      few_stream<MX ? 1 : 4, Step>(
           s0, n, steps, seek, load_w,
           [&](Step& S, int v, int step) {
             int p, t;
             column(v, &p, &t);
 #pragma unroll
             for (int i = 0; i < NB; ++i)
-              S.b[i] = few_fetch(hv + (size_t)p * (a.f / 8) + step * (KS / 8) + q4 * NB + i);
+              S.b[i] = hv[(size_t)p * (a.f / 8) + step * (KS / 8) + q4 * NB + i];
           },
           wait, [&](Step& S, int) { few_mfma<MX, 1>(S.w, S.s, S.b, acc); }, done);
     }
