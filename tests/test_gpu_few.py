@@ -26,6 +26,9 @@ SHAPES = {
     "e16-zipf": BASE.replace(E=16, d=384, bias="zipf"),
     "e64-presel": BASE.replace(E=64, presel=8, renorm=0, bias="normal", f=384),
     "e64-all": BASE.replace(E=64, k=4, renorm=0),
+    "e64-g16": BASE.replace(E=64, k=4, n_group=16, topk_group=3, d=128, f=128),
+    "e64-g32": BASE.replace(E=64, k=6, n_group=32, topk_group=5, d=128, f=128, bias="normal"),
+    "e64-presel32": BASE.replace(E=64, k=4, presel=32, renorm=0, d=128, f=128),
     "e256-grouped": BASE.replace(E=256, k=8, n_group=8, topk_group=4, f=128),
     "e96-g48": BASE.replace(E=96, k=4, n_group=48, topk_group=7, f=128),
     "e1024": BASE.replace(E=1024, k=16, d=128, f=128, renorm=0),

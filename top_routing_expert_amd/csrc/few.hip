@@ -352,7 +352,13 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_layer_kernel(FewArgs a) {
     }
   };
   using std::integral_constant;
-  if (a.E <= 64)
+  // With more tokens than waves, four tokens a wave where 16 lanes hold a token's choices and
+  // its gate sum: the lanes that are missing would add zeros, so the gates stay those of the
+  // wider groups (29 tokens of 64 experts: four rounds -> one, the layer 78 -> 74 us)
+  if (a.E <= 64 && T > kFewWaves && max(a.presel, k) <= 16 && a.n_group <= 16 &&
+      (a.renorm || a.presel))
+    select(integral_constant<int, 16>(), integral_constant<int, 4>());
+  else if (a.E <= 64)
     select(integral_constant<int, 64>(), integral_constant<int, 1>());
   else if (a.E <= 256 && a.n_group <= 32)
     select(integral_constant<int, 32>(), integral_constant<int, 8>());
