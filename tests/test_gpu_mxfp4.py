@@ -134,6 +134,21 @@ def test_payload_gather(T, d, E, k, bf):
     assert np.array_equal(out.double().cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("bf", [True, False])
+def test_large_payload_gather(bf):
+    """An x_perm large enough to be stored past the cache: the rows of the smaller decoding."""
+    T, d, k = (8192, 5120, 2) if bf else (4096, 5120, 2)
+    x = torch.randn((T, d), device="cuda").to(torch.bfloat16 if bf else torch.float32)
+    codes, scales = B.quantize_mxfp4(x)
+    src = torch.randperm(T * k, device="cuda").int()
+    cfg = _cfg(T, d, bf, E=8, k=k)
+    rows = torch.full((T, d), 3.0, dtype=x.dtype, device="cuda")
+    B.moe_dequantize_mxfp4(cfg, codes, None, scales, rows)
+    out = torch.full((T * k + 1, d), 3.0, dtype=x.dtype, device="cuda")
+    B.moe_dequantize_mxfp4(cfg, codes, src, scales, out)
+    assert torch.equal(out[:-1], rows[(src // k).long()]) and (out[-1] == 3.0).all()
+
+
 def test_quantize_helper_and_other_stream():
     x = torch.randn((5, 3, 256), dtype=torch.bfloat16, device="cuda")
     want = B.quantize_mxfp4(x)

@@ -273,3 +273,33 @@ def test_captured_backward_next_to_eager():
         torch.cuda.synchronize()
         for a, b in zip(o, want):
             assert torch.equal(a, b), i
+
+
+def test_stores_past_the_cache_write_the_same():
+    """Calls large enough to store past the cache, against the same tokens in four
+    calls that are not: every token's row is its own, so the bits are the same."""
+    T, d, k, parts = 5120, 7168, 8, 4
+    n = T // parts
+    log(f"[norm] combine T={T} d={d} k={k} in one call and in {parts}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    bf = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda").normal_(generator=g)  # noqa: E731
+    y, res, up, w, gate = bf(T * k, d), bf(T, d), bf(T, d), bf(d), bf(parts, d)
+    local = torch.cat([torch.randperm(n * k, device="cuda", generator=g) for _ in range(parts)]).int()
+    slot = (local.view(parts, -1) + torch.arange(parts, device="cuda").int()[:, None] * n * k).flatten()
+    tw = torch.rand((T, k), device="cuda", generator=g)
+
+    def run(cfg, y, slot, tw, res, gate, up):
+        t, q = res.shape[0], gate.shape[0]
+        o = [_new(t, d, bf=True), _new(t), _new(t * k, d, bf=True), _new(t, k), _new(t, d, bf=True)]
+        B.moe_combine_norm(cfg, y, slot, tw, res, w, gate, q, EPS, 0.5, o[0], o[1])
+        B.moe_combine_norm_backward(cfg, up, y, slot, tw, w, gate, q, 0.5, o[1], o[2], o[3], o[4],
+                                    None, None)
+        return o
+
+    whole = run(_cfg(T, d, True, k), y, slot, tw, res, gate, up)
+    for i in range(parts):
+        r, rk = slice(i * n, (i + 1) * n), slice(i * n * k, (i + 1) * n * k)
+        part = run(_cfg(n, d, True, k), y[rk], local[rk], tw[r], res[r], gate[i:i + 1], up[r])
+        for j, p in enumerate(part):
+            assert torch.equal(p, whole[j][rk if j == 2 else r]), (i, j)

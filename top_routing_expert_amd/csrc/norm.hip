@@ -62,6 +62,25 @@ struct Vec16<float> {
   }
 };
 
+// A combine that moves far more than the 256 MB Infinity Cache holds stores past it (past: the
+// same for every thread).  Measured with a reader of the output behind it, d = 7168, us:
+//   backward  T8192 k 8 (2.1 GB) 758 -> 734, T4096 k 8 (1.1 GB) 432 -> 406, T8192 k 2 (0.70 GB)
+//             263 -> 262; T1024 k 8 (0.26 GB), which stays ordinary, 139 -> 175
+//   forward   T8192 k 8 (1.2 GB) 258 -> 248; ordinary: T4096 k 8 (0.59 GB) 123 -> 123, T8192 k 2
+//             (0.47 GB) 117 -> 122
+// The norms in front of the block write less than they read and their readers come next: ordinary
+// (T16384-d5120, forward 82 -> 90 with its reader, backward 207 -> 210).
+constexpr long kNormPastBytes = 640L << 20;
+__device__ __forceinline__ void norm_store(u32x4* p, u32x4 v, bool past) {
+  if (past) {
+    asm volatile("");  // the compiler would make one ordinary store of the two
+    __builtin_nontemporal_store(v, p);
+    asm volatile("");
+  } else {
+    *p = v;
+  }
+}
+
 // Sum over the wave, the same value in every lane: moves within 16 lanes, then
 // swaps of 16- and 32-lane halves (a shuffle through LDS takes several times as
 // long a step).
@@ -308,7 +327,7 @@ __global__ __launch_bounds__(MAXT) void combine_norm_fwd_kernel(
     const u32x4* __restrict__ y, const int32_t* __restrict__ slot_of,
     const float* __restrict__ topk_w, const u32x4* residual, const u32x4* __restrict__ w,
     const u32x4* __restrict__ gate, int per_gate, float eps, float res_scale, u32x4* out,
-    float* __restrict__ rstd, int nvec, float inv_d, int rows, int k) {
+    float* __restrict__ rstd, int nvec, float inv_d, int rows, int k, bool past) {
   using V = Vec16<T>;
   constexpr int N = V::N;
   __shared__ float part[kNormMaxThreads / 64];
@@ -319,7 +338,7 @@ __global__ __launch_bounds__(MAXT) void combine_norm_fwd_kernel(
   float yf[VPT][N];
   float ss = 0.f;
   // vectors whose k rows are in flight together: at most 64 registers of rows
-  constexpr int BI = VPT * KC <= 16 ? VPT : 1;
+  constexpr int BI = VPT * KC <= 16 ? VPT : KC <= 8 ? 2 : 1;
   u32x4 res[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -355,6 +374,7 @@ __global__ __launch_bounds__(MAXT) void combine_norm_fwd_kernel(
 #pragma unroll
       for (int q = 0; q < N; ++q) ss = fmaf(yf[i][q], yf[i][q], ss);
     }
+    if constexpr (BI < VPT) asm volatile("" ::: "memory");  // the next rows are loaded here
   }
   const float r = 1.0f / sqrtf(norm_block_sum(ss, part) * inv_d + eps);
   if (rstd && threadIdx.x == 0) rstd[t] = r;
@@ -374,7 +394,7 @@ __global__ __launch_bounds__(MAXT) void combine_norm_fwd_kernel(
         if (gate) n *= gf[q];
         o[q] = residual ? fmaf(res_scale, rf[q], n) : n;
       }
-      out[(size_t)t * nvec + v] = V::pack(o);
+      norm_store(out + (size_t)t * nvec + v, V::pack(o), past);
     }
   }
 }
@@ -392,7 +412,7 @@ __global__ __launch_bounds__(MAXT) void combine_norm_bwd_kernel(
     const u32x4* __restrict__ w, const u32x4* __restrict__ gate, int per_gate, float res_scale,
     const float* __restrict__ rstd, u32x4* __restrict__ d_y, float* __restrict__ d_topk_w,
     u32x4* __restrict__ d_residual, float* __restrict__ partial, int nvec, float inv_d, int rows,
-    int k, int T_, int per) {
+    int k, int T_, int per, bool past) {
   using V = Vec16<T>;
   constexpr int N = V::N;
   __shared__ float part[2][kNormMaxThreads / 64];
@@ -468,7 +488,7 @@ __global__ __launch_bounds__(MAXT) void combine_norm_bwd_kernel(
         S[i][q] = fmaf(df[q], n[i][q], S[i][q]);
         o[q] = res_scale * df[q];
       }
-      if (d_residual) d_residual[(size_t)t * nvec + v] = V::pack(o);
+      if (d_residual) norm_store(d_residual + (size_t)t * nvec + v, V::pack(o), past);
       upstream(i, v, dn);
 #pragma unroll
       for (int q = 0; q < N; ++q) dot = fmaf(dn[q], n[i][q], dot);
@@ -510,7 +530,7 @@ __global__ __launch_bounds__(MAXT) void combine_norm_bwd_kernel(
             if (d_topk_w) dw[j] = fmaf(dy[q], f[q], dw[j]);
             o[q] = g[j] * dy[q];
           }
-          d_y[(size_t)p[j] * nvec + v] = V::pack(o);
+          norm_store(d_y + (size_t)p[j] * nvec + v, V::pack(o), past);
         }
       }
     }
@@ -637,6 +657,10 @@ size_t combine_norm_backward_ws_bytes(const moe_config& c, int n_gate) {
 // Threads of a row: two vectors each up to 1024 vectors, four above.
 static int norm_threads(int nvec, int vpt) { return div_up(div_up(nvec, vpt), 64) * 64; }
 static bool norm_small(int nvec) { return nvec <= 1024; }
+// Whether a call that moves `rows` rows of d elements stores past the cache.
+static bool norm_past(const moe_config& c, long rows) {
+  return rows * norm_nvec(c) * 16 > kNormPastBytes;
+}
 
 template <typename F>
 static void with_types(const moe_config& c, F&& f) {
@@ -735,6 +759,7 @@ hipError_t launch_combine_norm(const moe_config& c, const void* y, const int32_t
   const auto* gv = static_cast<const u32x4*>(gate);
   auto* ov = static_cast<u32x4*>(out);
   const float inv_d = 1.0f / (float)c.d;
+  const bool past = norm_past(c, (long)rows + (residual ? 2L : 1L) * c.T);
   with_types(c, [&](auto t) {
     using T = decltype(t);
     with_k(k, [&](auto kc) {
@@ -742,11 +767,11 @@ hipError_t launch_combine_norm(const moe_config& c, const void* y, const int32_t
       if (norm_small(nvec))
         combine_norm_fwd_kernel<T, 2, 512, KC><<<c.T, norm_threads(nvec, 2), 0, st>>>(
             yv, slot_of, topk_w, rv, wv, gv, per_gate, eps, res_scale, ov, rstd, nvec, inv_d, rows,
-            k);
+            k, past);
       else
         combine_norm_fwd_kernel<T, 4, 512, KC><<<c.T, norm_threads(nvec, 4), 0, st>>>(
             yv, slot_of, topk_w, rv, wv, gv, per_gate, eps, res_scale, ov, rstd, nvec, inv_d, rows,
-            k);
+            k, past);
     });
   });
   return hipGetLastError();
@@ -773,6 +798,7 @@ hipError_t launch_combine_norm_backward(const moe_config& c, const void* d_out, 
   auto* drv = static_cast<u32x4*>(d_residual);
   float* partial = d_w || d_gate ? static_cast<float*>(ws) : nullptr;
   const float inv_d = 1.0f / (float)c.d;
+  const bool past = norm_past(c, 2L * rows + (d_residual ? 2L : 1L) * c.T);
   with_types(c, [&](auto t) {
     using T = decltype(t);
     with_k(k, [&](auto kc) {
@@ -781,12 +807,14 @@ hipError_t launch_combine_norm_backward(const moe_config& c, const void* d_out, 
         combine_norm_bwd_kernel<T, 2, 512, KC, (KC <= 8)>
             <<<blocks, norm_threads(nvec, 2), 0, st>>>(dv, yv, slot_of, topk_w, wv, gv, per_gate,
                                                        res_scale, rstd, dyv, d_topk_w, drv,
-                                                       partial, nvec, inv_d, rows, k, c.T, per);
+                                                       partial, nvec, inv_d, rows, k, c.T, per,
+                                                       past);
       else
         combine_norm_bwd_kernel<T, 4, 512, KC, false>
             <<<blocks, norm_threads(nvec, 4), 0, st>>>(dv, yv, slot_of, topk_w, wv, gv, per_gate,
                                                        res_scale, rstd, dyv, d_topk_w, drv,
-                                                       partial, nvec, inv_d, rows, k, c.T, per);
+                                                       partial, nvec, inv_d, rows, k, c.T, per,
+                                                       past);
     });
   });
   hipError_t e = hipGetLastError();
