@@ -74,6 +74,15 @@ struct MxTile {
   static_assert((STAGES - 1) * DPW + GPW <= 63, "vmcnt range");
 };
 
+// Four features each of groups g (a) and g + 1 (b) of a token, the first four of a group in
+// lanes 0..31 and the next four in lanes 32..63 -> all eight of g in lanes 0..31 and of
+// g + 1 in lanes 32..63, for one 16-byte store.
+__device__ __forceinline__ u32x4 mx_join(u32x2 a, u32x2 b) {
+  const auto x = __builtin_amdgcn_permlane32_swap(a.x, b.x, false, false);
+  const auto y = __builtin_amdgcn_permlane32_swap(a.y, b.y, false, false);
+  return u32x4{x[0], y[0], x[1], y[1]};
+}
+
 template <bool GATED, int GW, int GT, int WA, int WB, int STAGES, int BLOCKS, bool S4>
 __global__ __launch_bounds__(64 * GW * GT, BLOCKS * GW * GT / 4) void mxfp4_gemm_kernel(
     const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
@@ -363,6 +372,7 @@ __global__ __launch_bounds__(64 * GW * GT, BLOCKS * GW * GT / 4) void mxfp4_gemm
         const int prf = t.pr0 + wn * 32 * WA + 32 * i;  // first packed row of the fragment
         if (prf >= R) continue;
         if constexpr (GATED) {  // rows 0..15 gate, 16..31 up of the same 16 features
+          u32x2 pk[2];
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             float hv[4];
@@ -371,18 +381,22 @@ __global__ __launch_bounds__(64 * GW * GT, BLOCKS * GW * GT / 4) void mxfp4_gemm
               const float a = acc[i][j][4 * g + r], u = acc[i][j][4 * g + 8 + r];
               hv[r] = a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)) * u;
             }
-            u32x2 pk;
-            pk.x = pack_bf16x2(hv[0], hv[1]);
-            pk.y = pack_bf16x2(hv[2], hv[3]);
-            *reinterpret_cast<u32x2*>(out + (size_t)p * N + prf / 2 + 8 * g + 4 * lk) = pk;
+            pk[g].x = pack_bf16x2(hv[0], hv[1]);
+            pk[g].y = pack_bf16x2(hv[2], hv[3]);
           }
+          *reinterpret_cast<u32x4*>(out + (size_t)p * N + prf / 2 + 8 * lk) = mx_join(pk[0], pk[1]);
         } else {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            u32x2 pk;
-            pk.x = pack_bf16x2(acc[i][j][4 * g], acc[i][j][4 * g + 1]);
-            pk.y = pack_bf16x2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
-            *reinterpret_cast<u32x2*>(out + (size_t)p * N + prf + 8 * g + 4 * lk) = pk;
+          for (int g = 0; g < 4; g += 2) {
+            u32x2 pk[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int r = 4 * (g + h);
+              pk[h].x = pack_bf16x2(acc[i][j][r], acc[i][j][r + 1]);
+              pk[h].y = pack_bf16x2(acc[i][j][r + 2], acc[i][j][r + 3]);
+            }
+            *reinterpret_cast<u32x4*>(out + (size_t)p * N + prf + 8 * (g + lk)) =
+                mx_join(pk[0], pk[1]);
           }
         }
       }
