@@ -698,6 +698,10 @@ int moe_norm_backward(const moe_config* cfg, const void* d_xn, const void* x, co
  *                                            with slot_of NULL)
  *   d_topk_w[t,j] = <dy, y[slot_of[t*k+j]]>  [T, k] float32 out or NULL (must be
  *                                            NULL with slot_of NULL)
+ *                                            With k = 1 the norm cancels the
+ *                                            weight: what is left is eps' share,
+ *                                            the difference of equal terms, and
+ *                                            as uncertain as the rounding of rstd.
  *   d_residual = residual_scale d_out        [T, d] (dtype) out or NULL
  *   d_weight = sum_t gate d_out n            [d] float32 out or NULL
  *   d_gate[q] = weight sum of d_out n over the tokens of row q

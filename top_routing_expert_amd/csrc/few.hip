@@ -39,6 +39,12 @@
 //    chunks, decoded to bf16 in registers by v_cvt_scalef32_pk_bf16_fp4).  x
 //    and h are kept in LDS where they fit, so that the registers in flight hold
 //    weights only.
+//
+// Measured (a pass, both kernels): T1-d7168-E256 top-8 f2048 134 us, 5.3 TB/s of weights: bound
+// by HBM.  T1-d5120-E16 top-2 f1536 32 us for 95 MB: logits 5 us, selection 2 us, the hand-over of
+// h 2..3 us, the rest the streams' first latencies and 3..4 TB/s.  T29-d2048-E64 top-2 f1408
+// MXFP4 71 us for 178 MB: selection and lists 6 us, gate / up 30 us, down 22 us, where neither
+// all of x nor of h fits in LDS and a 16-row step decodes as long as it loads.
 #include <algorithm>
 
 #include "mxfp4.h"

@@ -17,6 +17,11 @@
 // that d_topk_w needs anyway.  The backward's parameter gradients are summed
 // in registers over a block's tokens, written as float32 partial rows and
 // added by a second kernel in a fixed order (no atomics).
+//
+// All bound by HBM: T16383-d5120 forward 59 us and backward 142 us (5.7 and 4.7 TB/s), the
+// parameter gradient 6.6 us behind it; with T8192-d7168 k 8 the combine forward and
+// backward take 658 us for 3.3 GB.  One block a row needs no second pass; two rows a block
+// or persistent forward blocks would share nothing but the weight row, which stays in L2.
 #include <algorithm>
 #include <type_traits>
 
