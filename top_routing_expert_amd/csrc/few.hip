@@ -43,7 +43,7 @@
 // Measured (a pass, both kernels): T1-d7168-E256 top-8 f2048 134 us, 5.3 TB/s of weights: bound
 // by HBM.  T1-d5120-E16 top-2 f1536 32 us for 95 MB: logits 5 us, selection 2 us, the hand-over of
 // h 2..3 us, the rest the streams' first latencies and 3..4 TB/s.  T29-d2048-E64 top-2 f1408
-// MXFP4 71 us for 178 MB: selection and lists 6 us, gate / up 30 us, down 22 us, where neither
+// MXFP4 71 us for 178 MB: logits 6 us, selection and lists 9, gate / up 32, down 22, where neither
 // all of x nor of h fits in LDS and a 16-row step decodes as long as it loads.
 #include <algorithm>
 

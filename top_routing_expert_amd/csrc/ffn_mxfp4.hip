@@ -26,10 +26,10 @@
 // of which its MFMAs fill 0.43: bound by the copies into LDS (33 KB a stage and CU,
 // 7..8 TB/s over the chip) and the fragment reads beside them.  Measured, products alone:
 // T8192-d7168-E64 top-8 f2048 gate / up 1140 us (3.4 PFLOP/s; 256 x 128 1331, 128 x 256
-// 1455, 128 x 128 on four or eight waves 1818 and 1695), T1024-d4096-E8 top-2 f11008 down 84 us
-// (101, 110, 135, 125).  Below 128 rows an expert 128 x 64, two blocks a CU: the weights are
-// read once whatever the tile, and more blocks read them together (T37-E16 23 us, 5.8
-// TB/s; 256 x 256 leaves most CUs without a tile).
+// 1455, 128 x 128 on four or eight waves 1818 and 1695), T1024-d4096-E8 top-2 f11008 down
+// 84 us (101, 110, 135, 125; 104 with the weights from HBM).  Below 128 rows an expert
+// 128 x 64, two blocks a CU: the weights are read once whatever the tile, and more blocks
+// read them together (T37-d5120-E16 23 us, 5.8 TB/s).
 #include <algorithm>
 #include <type_traits>
 

@@ -11,8 +11,8 @@
 //   exchange their maxima.
 // dequantize: thread per 8 elements of an expert-ordered row p: codes and scale of
 //   token src_of[p] / k (or of row p itself), values exact in bf16.
-// Both are bound by HBM: T16384-d5120 quantised in 41 us, 5.2 TB/s of 213 MB, and its 32768
-// rows of top-2 decoded in 50 us.
+// Both are bound by HBM: T16384-d5120 quantised in 29..49 us (213 MB, as far as x is in the
+// Infinity Cache), its 32768 rows of top-2 decoded in 61 us (380 MB, 6.3 TB/s).
 #include "mxfp4.h"
 
 namespace moe {
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const u32x4* __restric
 // groups of 8 elements a thread, their loads in flight together.  past (the same for every
 // thread): x_perm is stored past the 256 MB Infinity Cache, from kMxPastBytes of it on.
 // Measured with the combine that reads it behind, k = 2, d = 5120: T16384 (335 MB) 177 -> 143
-// us, T8192 77 -> 75, T4096 40 -> 41; T16384 alone 84 -> 42.
+// us, T8192 77 -> 75, T4096 40 -> 41; the decoding of T16384 alone 84 -> 61.
 constexpr long kMxPastBytes = 128L << 20;
 template <bool BF16, int U>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(

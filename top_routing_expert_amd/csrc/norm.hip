@@ -20,8 +20,7 @@
 //
 // All bound by HBM: T16383-d5120 forward 59 us and backward 142 us (5.7 and 4.7 TB/s), the
 // parameter gradient 6.6 us behind it; with T8192-d7168 k 8 the combine forward and
-// backward take 658 us for 3.3 GB.  One block a row needs no second pass; two rows a block
-// or persistent forward blocks would share nothing but the weight row, which stays in L2.
+// backward take 201 and 456 us for 3.3 GB (5 TB/s), the parameter gradients 7 us.
 #include <algorithm>
 #include <type_traits>
 
