@@ -200,3 +200,24 @@ def test_empty_batch():
     cfg = B.config(BASE, T=0)
     assert B.workspace(cfg, "layer_few") is None
     B.moe_layer_fwd_few(cfg, None, None, None, None, None, 0, None)
+
+
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp4"])
+def test_non_finite_tokens_stay_to_themselves(mx):
+    """Tokens of NaN and infinities choose experts in range, and no other token's
+    routing or output moves by more than the order of its sums."""
+    shape = SHAPES["e16-zipf"].replace(T=20)
+    inp = I.make_inputs(shape, 8)
+    dev = upload(inp)
+    images, vals = _images(shape, inp, dev, mx)
+    bad = [3, 7, 19]
+    good = [t for t in range(shape.T) if t not in bad]
+    dev["x"][3], dev["x"][7, 5], dev["x"][19] = float("nan"), float("inf"), float("-inf")
+    out, b = _run(shape, dev, images, mx)
+    idx = host(b["topk_idx"])
+    assert ((idx >= 0) & (idx < shape.E)).all() and (idx[:, 0] != idx[:, 1]).all()
+    assert all(torch.isnan(out[t]).any() for t in bad)
+    ref = oracle.layer(inp["x"], inp["w_router"], inp["bias"], vals["w_gate"], vals["w_up"],
+                       vals["w_down"], k=shape.k, renorm=shape.renorm)
+    assert np.array_equal(idx[good], ref["topk_idx"][good])
+    assert rel_err(oracle.widen_bf16(host(out[:shape.T]))[good], ref["out"][good]) <= TOL_LAYER["bf16"]

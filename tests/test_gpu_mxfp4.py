@@ -323,3 +323,27 @@ def test_products_captured_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want), i
+
+
+@pytest.mark.parametrize("rows_per", [3, 200])
+def test_non_finite_rows_stay_to_themselves(rows_per):
+    """A block with a NaN makes its own row NaN and changes no bit of another."""
+    rng = np.random.default_rng(rows_per)
+    E, K, N = 3, 512, 256
+    rows = E * rows_per
+    offs = np.arange(E + 1, dtype=np.int32) * rows_per
+    wc, ws = _weights(rng, E, N, K, False)
+    hc, hs = _acts(rng, rows, K, False)
+    cfg = B.config(T=rows, d=N, E=E, k=1, f=K)
+    _, image = B.pack_weights_mxfp4(cfg, None, None, _dev(wc, ws))
+    c, s, o = _dev(hc, hs, offs)
+    clean = torch.zeros((rows, N), dtype=torch.bfloat16, device="cuda")
+    B.moe_ffn_down_mxfp4(cfg, c, s, o, image, clean)
+    assert torch.isfinite(clean).all()
+    bad = [1, rows_per + 2, rows - 1]
+    for i, r in enumerate(bad):
+        s[r, 3 + i] = 255
+    got = torch.zeros_like(clean)
+    B.moe_ffn_down_mxfp4(cfg, c, s, o, image, got)
+    rest = [r for r in range(rows) if r not in bad]
+    assert torch.isnan(got[bad]).all() and torch.equal(got[rest], clean[rest])
